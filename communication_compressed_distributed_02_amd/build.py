@@ -11,7 +11,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libob_adam.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip")]
+SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
+                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
          "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",
@@ -20,7 +21,8 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
 
 
 PROBE_LIB = os.path.join(PKG, "libob_probe.so")
-PROBE_SOURCES = [os.path.join(CSRC, "ob_probe.hip")]
+PROBE_SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
+                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
 
 
 def build(extra_flags=(), out=LIB):
@@ -40,7 +42,8 @@ def build_probe(out=PROBE_LIB):
 
 
 MATHCHECK_LIB = os.path.join(PKG, "libob_mathcheck.so")
-MATHCHECK_SOURCES = [os.path.join(CSRC, "ob_mathcheck.hip")]
+MATHCHECK_SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
+                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
 
 
 def build_mathcheck(out=MATHCHECK_LIB):

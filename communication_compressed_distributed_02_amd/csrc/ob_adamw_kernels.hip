@@ -1,0 +1,724 @@
+// gfx950 kernels of AdamW's step over many tensors and of the gradient norm.
+// The arithmetic contract is stated in include/ob_adamw.h.
+//
+// Mapping: a block of 4 waves owns a chunk of 4096 elements of one tensor, a
+// wave a row of 1024 of them, and a lane 4 consecutive elements of each of
+// the row's 4 groups of 256.  A group is the unit that shares the exponents of
+// an 8-bit state, so its maximum is a reduction over one wave's lanes, in
+// registers.  The list of chunks (tensor, place, length, group) is made once
+// per plan; the tensors' pointers come by value with each launch.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "ob_adamw_kernels.h"
+
+namespace ob {
+namespace adamw {
+namespace {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kGroups = kRowElems / kScaleElems;  // groups of 256 in a wave's row
+
+struct bf16 {
+  uint16_t bits;
+};
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(bf16 x) { return __uint_as_float((uint32_t)x.bits << 16); }
+
+// Two fp32 values as bfloat16, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const bf16x2 h = __builtin_convertvector(f32x2{a, b}, bf16x2);
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+template <typename T>
+__device__ __forceinline__ T ld_stream(const T* p) { return __builtin_nontemporal_load(p); }
+template <typename T>
+__device__ __forceinline__ void st_stream(T* p, T v) { __builtin_nontemporal_store(v, p); }
+
+// Four elements from p, where p is aligned to four of them.
+__device__ __forceinline__ f32x4 load4(const float* p) { return ld_stream((const f32x4*)p); }
+__device__ __forceinline__ f32x4 load4(const bf16* p) {
+  const u32x2 w = ld_stream((const u32x2*)p);
+  return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+               __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
+}
+// The first n (0 to 4) of them at element alignment, zeros after.
+template <typename T>
+__device__ __forceinline__ f32x4 load_some(const T* p, int n) {
+  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (k < n) r[k] = widen(p[k]);
+  return r;
+}
+
+// Random bits: a 32-bit word hashed from the quad's index and the step's
+// first key, and more words from the word before and the second key.  The
+// multipliers are digits of sqrt(5), sqrt(3) and the golden ratio; every
+// input bit flips every output bit with probability 1/2 within the noise of
+// 65536 quads, and no two bits of the four words correlate above it.
+__device__ __forceinline__ uint32_t first_word(uint32_t quad, uint32_t key) {
+  uint32_t h = quad ^ key;
+  h = (h ^ (h >> 16)) * 0x3C6EF373u;
+  h = (h ^ (h >> 15)) * 0xBB67AE85u;
+  return h ^ (h >> 16);
+}
+__device__ __forceinline__ uint32_t next_word(uint32_t word, uint32_t key, uint32_t i) {
+  const uint32_t h = (word ^ key) * 0x9E3779B9u + i;
+  return h ^ (h >> 15);
+}
+// Quads past 2^32 take another key.
+__device__ __forceinline__ uint32_t high_key(uint64_t quad, uint32_t key) {
+  return key ^ ((uint32_t)(quad >> 32) * 0x9E3779B9u);
+}
+__device__ __forceinline__ uint32_t random16(uint32_t a, uint32_t b, int k) {
+  const uint32_t w = k < 2 ? a : b;
+  return k & 1 ? w >> 16 : w & 0xffffu;
+}
+
+// The low 16 bits of x's fp32 pattern rounded stochastically away.  What is
+// not finite keeps its pattern (an arithmetic NaN has its quiet bit above).
+__device__ __forceinline__ uint32_t round_stochastic(float x, uint32_t r16) {
+  const uint32_t b = __float_as_uint(x);
+  return (b & 0x7f800000u) == 0x7f800000u ? b : b + r16;
+}
+
+// Largest value over the wave's 64 lanes, as a scalar: four shifts within
+// rows of 16 lanes, then row 0 and 2's last lane to the next row, then lane 31
+// to the upper half; lane 63 ends with all of them.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  const auto step = [&](auto ctrl, auto rows) {
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)x, decltype(ctrl)::value, decltype(rows)::value, 0xf, false);
+    x = y > x ? y : x;
+  };
+  step(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());  // row_shr:1
+  step(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());  // row_shr:2
+  step(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());  // row_shr:4
+  step(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());  // row_shr:8
+  step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());  // row_bcast:15
+  step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());  // row_bcast:31
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+__device__ __forceinline__ bool finite_bits(uint32_t b) { return (b & 0x7f800000u) != 0x7f800000u; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t umin(uint32_t a, uint32_t b) { return a < b ? a : b; }
+
+// ---------------------------------------------------------- 8-bit codes --
+// First moment, a group's four elements of this lane.  e: the group's
+// exponent byte; scaling by a power of two is exact, so the e4m3 conversion
+// is the only rounding.
+__device__ __forceinline__ f32x4 decode_m(uint32_t codes, uint32_t e) {
+  const float s = __uint_as_float((e - 7u) << 23);
+  const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, false);
+  const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, true);
+  return f32x4{lo.x * s, lo.y * s, hi.x * s, hi.y * s};
+}
+
+// Codes and exponent of a group whose elements lane by lane are m.
+__device__ __forceinline__ uint32_t encode_m(f32x4 m, uint32_t* e_out) {
+  uint32_t a[4], top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    a[k] = __float_as_uint(m[k]) & 0x7fffffffu;
+    top = umax(top, a[k]);
+  }
+  uint32_t e = wave_max(top) >> 23;
+  if (e == 255u) {  // something is not finite: held as NaN, the others keep their scale
+    top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (finite_bits(a[k])) top = umax(top, a[k]);
+      else m[k] = __uint_as_float(0x7fc00000u);
+    }
+    e = wave_max(top) >> 23;
+  }
+  e = umax(e, (uint32_t)kMinExpM);
+  const float s = __uint_as_float((261u - e) << 23);
+  int c = __builtin_amdgcn_cvt_pk_fp8_f32(m.x * s, m.y * s, 0, false);
+  c = __builtin_amdgcn_cvt_pk_fp8_f32(m.z * s, m.w * s, c, true);
+  *e_out = e;
+  return (uint32_t)c;
+}
+
+// Second moment: the code counts eighths of a binade up from the group's
+// floor, so decoding is an addition to the fp32 pattern's upper bits.
+__device__ __forceinline__ uint32_t floor_v(uint32_t e) { return (e - 31u) * 8u + 1u; }
+
+__device__ __forceinline__ f32x4 decode_v(uint32_t codes, uint32_t e) {
+  const uint32_t low = floor_v(e);
+  f32x4 v;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t c = (codes >> (8 * k)) & 255u;
+    uint32_t b = c == 0 ? 0u : (c + low) << 20;
+    if (c == 255u) b = 0x7fc00000u;
+    v[k] = __uint_as_float(b);
+  }
+  return v;
+}
+
+// noise(k): what is added to element k's pattern before its low 20 bits go.
+template <typename N>
+__device__ __forceinline__ uint32_t encode_v(f32x4 v, uint32_t* e_out, N noise) {
+  uint32_t q[4], top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    q[k] = (__float_as_uint(v[k]) + noise(k)) >> 20;
+    top = umax(top, q[k]);
+  }
+  top = wave_max(top);
+  uint32_t odd = 0;  // bit k: element k is not finite
+  if (top >= 2040u) {  // something is not finite, or the largest fp32 values round up to infinity
+    top = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (finite_bits(__float_as_uint(v[k]))) {
+        q[k] = umin(q[k], 2039u);
+        top = umax(top, q[k]);
+      } else {
+        odd |= 1u << k;
+      }
+    }
+    top = wave_max(top);
+  }
+  const uint32_t e = umax(top >> 3, (uint32_t)kMinExpV);
+  const int low = (int)floor_v(e);
+  uint32_t codes = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    int c = (int)q[k] - low;
+    c = c < 1 ? 1 : (c > 254 ? 254 : c);
+    if (v[k] == 0.0f) c = 0;
+    if ((odd >> k) & 1u) c = 255;
+    codes |= (uint32_t)c << (8 * k);
+  }
+  *e_out = e;
+  return codes;
+}
+
+// ------------------------------------------------------------------ step --
+__device__ __forceinline__ float moment1(float m, float g, float b1, float ob1) {
+  return (b1 * m) + (ob1 * g);
+}
+__device__ __forceinline__ float moment2(float v, float g, float b2, float ob2) {
+  return (b2 * v) + (ob2 * (g * g));
+}
+__device__ __forceinline__ float updated(float x, float m, float v, float decay, float rate,
+                                         float rbc2, float eps) {
+  const float den = (sqrtf(v) * rbc2) + eps;
+  return (x * decay) - (rate * (m / den));
+}
+
+template <typename PT, bool SR>
+__device__ __forceinline__ void store_param(PT* p, f32x4 x, int n, bool whole, uint32_t a,
+                                            uint32_t b) {
+  if constexpr (sizeof(PT) == 4) {
+    if (whole) {
+      st_stream((f32x4*)p, x);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < n) p[k] = x[k];
+    }
+  } else {
+    u32x2 w;
+    if constexpr (SR) {
+      uint32_t s[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] = round_stochastic(x[k], random16(a, b, k));
+      w = u32x2{(s[0] >> 16) | (s[1] & 0xffff0000u), (s[2] >> 16) | (s[3] & 0xffff0000u)};
+    } else {
+      w = u32x2{pack_bf16(x.x, x.y), pack_bf16(x.z, x.w)};
+    }
+    if (whole) {
+      st_stream((u32x2*)p, w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < n) p[k].bits = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+    }
+  }
+}
+
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
+__global__ void __launch_bounds__(kBlock)
+    step_kernel(StepPtrs ptrs, State s, uint32_t t0, int64_t c0) {
+  const Control* __restrict__ ctl = s.control;
+  if (ctl->skip) return;
+  const ChunkRec rec = s.recs[c0 + blockIdx.x];
+  const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
+  PT* p = (PT*)ptrs.p[rec.tensor - t0];
+  if (g == nullptr) return;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = threadIdx.x & 63;
+  const int left = (int)rec.count - wave * kRowElems;  // elements from this wave's row on
+  if (left <= 0) return;
+  const int64_t row = (int64_t)rec.row + wave;
+  const int64_t srow = (int64_t)rec.state_row + wave;
+  g += row * kRowElems;
+  p += row * kRowElems;
+  const bool whole = left >= kRowElems && ((uintptr_t)g & (4 * sizeof(GT) - 1)) == 0 &&
+                     ((uintptr_t)p & (4 * sizeof(PT) - 1)) == 0;
+  const int at = lane * 4;
+  f32x4 gv[kGroups], xv[kGroups], mv[kGroups], vv[kGroups];
+  uint32_t mc[kGroups], vc[kGroups], me = 0, ve = 0;
+  float* master = MASTER ? s.master + srow * kRowElems : nullptr;
+  float* m32 = (float*)s.m + srow * kRowElems;
+  float* v32 = (float*)s.v + srow * kRowElems;
+  uint8_t* m8 = (uint8_t*)s.m + srow * kRowElems;
+  uint8_t* v8 = (uint8_t*)s.v + srow * kRowElems;
+  if (whole) {
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) gv[u] = load4(g + u * kScaleElems + at);
+    if constexpr (!MASTER) {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) xv[u] = load4(p + u * kScaleElems + at);
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) gv[u] = load_some(g + u * kScaleElems + at,
+                                                        left - u * kScaleElems - at);
+    if constexpr (!MASTER) {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) xv[u] = load_some(p + u * kScaleElems + at,
+                                                          left - u * kScaleElems - at);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) {
+    if constexpr (MASTER) xv[u] = load4(master + u * kScaleElems + at);
+    if constexpr (BITS == 32) {
+      mv[u] = load4(m32 + u * kScaleElems + at);
+      vv[u] = load4(v32 + u * kScaleElems + at);
+    } else {
+      mc[u] = ld_stream((const uint32_t*)(m8 + u * kScaleElems + at));
+      vc[u] = ld_stream((const uint32_t*)(v8 + u * kScaleElems + at));
+    }
+  }
+  if constexpr (BITS == 8) {
+    me = *(const uint32_t*)(s.m_exp + srow * kGroups);
+    ve = *(const uint32_t*)(s.v_exp + srow * kGroups);
+  }
+  const float gs = ctl->gscale, rbc2 = ctl->rbc2;
+  const float decay = ctl->decay[rec.group], rate = ctl->rate[rec.group];
+  const float ob1 = 1.0f - s.beta1, ob2 = 1.0f - s.beta2;
+  uint32_t key0 = 0, key1 = 0;
+  const uint64_t quad0 = (uint64_t)srow * (kRowElems / 4);
+  if constexpr (BITS == 8 || SR) {
+    key0 = high_key(quad0, ctl->k0);
+    key1 = ctl->k1;
+  }
+  uint32_t new_me = 0, new_ve = 0;
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) {
+    if constexpr (BITS == 8) {
+      mv[u] = decode_m(mc[u], (me >> (8 * u)) & 255u);
+      vv[u] = decode_v(vc[u], (ve >> (8 * u)) & 255u);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float gk = gv[u][k] * gs;
+      mv[u][k] = moment1(mv[u][k], gk, s.beta1, ob1);
+      vv[u][k] = moment2(vv[u][k], gk, s.beta2, ob2);
+      xv[u][k] = updated(xv[u][k], mv[u][k], vv[u][k], decay, rate, rbc2, s.eps);
+    }
+    const int n = left - u * kScaleElems - at;
+    if (!whole) {  // what lies behind the tensor's last element stays zero
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k >= n) mv[u][k] = vv[u][k] = xv[u][k] = 0.0f;
+    }
+    uint32_t w0 = 0, w1 = 0, w2 = 0, w3 = 0;
+    if constexpr (BITS == 8 || SR) {
+      w0 = first_word((uint32_t)quad0 + u * (kScaleElems / 4) + lane, key0);
+      w1 = next_word(w0, key1, 1);
+    }
+    if constexpr (SR) {
+      w2 = next_word(w1, key1, 2);
+      w3 = next_word(w2, key1, 3);
+    }
+    store_param<PT, SR>(p + u * kScaleElems + at, xv[u], n, whole, w2, w3);
+    if constexpr (MASTER) st_stream((f32x4*)(master + u * kScaleElems + at), xv[u]);
+    if constexpr (BITS == 32) {
+      st_stream((f32x4*)(m32 + u * kScaleElems + at), mv[u]);
+      st_stream((f32x4*)(v32 + u * kScaleElems + at), vv[u]);
+    } else {
+      uint32_t e;
+      const uint32_t cm = encode_m(mv[u], &e);
+      new_me |= e << (8 * u);
+      const uint32_t cv = encode_v(vv[u], &e, [&](int k) {
+        return (random16(w0, w1, k) << 4) | 8u;
+      });
+      new_ve |= e << (8 * u);
+      st_stream((uint32_t*)(m8 + u * kScaleElems + at), cm);
+      st_stream((uint32_t*)(v8 + u * kScaleElems + at), cv);
+    }
+  }
+  if constexpr (BITS == 8) {
+    if (lane == 0) {
+      *(uint32_t*)(s.m_exp + srow * kGroups) = new_me;
+      *(uint32_t*)(s.v_exp + srow * kGroups) = new_ve;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ norm --
+// The block's sum in a fixed order: lanes by an xor butterfly, then the four
+// waves.
+__device__ __forceinline__ double block_sum(double acc, double* red) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) acc = acc + __shfl_xor(acc, o, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+template <typename GT>
+__global__ void __launch_bounds__(kBlock)
+    norm_kernel(NormPtrs ptrs, const ChunkRec* __restrict__ recs, uint32_t t0, int64_t c0,
+                int64_t n, double* __restrict__ partials) {
+  __shared__ double red[kBlock / 64];
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int at = (threadIdx.x & 63) * 4;
+  double acc = 0.0;
+  for (int64_t c = blockIdx.x; c < n; c += gridDim.x) {
+    const ChunkRec rec = recs[c0 + c];
+    const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
+    const int left = (int)rec.count - wave * kRowElems;
+    if (g == nullptr || left <= 0) continue;
+    g += ((int64_t)rec.row + wave) * kRowElems;
+    f32x4 v[kGroups];
+    if (left >= kRowElems && ((uintptr_t)g & (4 * sizeof(GT) - 1)) == 0) {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) v[u] = load4(g + u * kScaleElems + at);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) v[u] = load_some(g + u * kScaleElems + at,
+                                                         left - u * kScaleElems - at);
+    }
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const double d = (double)v[u][k];  // the square is exact in fp64
+        acc = __builtin_fma(d, d, acc);
+      }
+    }
+  }
+  acc = block_sum(acc, red);
+  if (threadIdx.x == 0) partials[blockIdx.x] = acc;
+}
+
+// Sum of n partials by one block, in an order fixed by n.
+__device__ __forceinline__ double fold_partials(const double* partials, int64_t n, double* red) {
+  double acc = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += kBlock) acc = acc + partials[i];
+  return block_sum(acc, red);
+}
+
+__global__ void __launch_bounds__(kBlock)
+    norm_finish_kernel(const double* __restrict__ partials, int64_t n, float grad_scale,
+                       double* sumsq, float* norm) {
+  __shared__ double red[kBlock / 64];
+  const double total = fold_partials(partials, n, red);
+  if (threadIdx.x != 0) return;
+  if (sumsq != nullptr) *sumsq = total;
+  if (norm != nullptr) *norm = (float)(sqrt(total) * (double)grad_scale);
+}
+
+__device__ __forceinline__ uint64_t mix64(uint64_t z, uint64_t mul) {
+  z ^= z >> 31;
+  return z * mul;
+}
+
+// One block: S, the clipping factor, the step count and the scalars of the
+// step that follows on the stream.
+__global__ void __launch_bounds__(kBlock) control_kernel(Control* c, ControlArgs a) {
+  __shared__ double red[kBlock / 64];
+  double total = 0.0;
+  if (a.partials != nullptr) {
+    total = fold_partials(a.partials, a.n_partials, red);
+  } else if (a.sumsq != nullptr) {
+    total = *a.sumsq;
+  }
+  const double norm = sqrt(total) * (double)a.grad_scale;
+  const bool skip = a.skip_nonfinite && !(total <= 1.7976931348623157e308);
+  const double p1 = c->p1 * (double)a.beta1, p2 = c->p2 * (double)a.beta2;
+  const int64_t t = c->steps + 1;
+  __syncthreads();  // every thread has read them before thread 0 writes
+  if (!skip && (int)threadIdx.x < a.n_groups) {
+    const int i = threadIdx.x;
+    const double lr = (double)(a.lr_device != nullptr ? a.lr_device[i] : a.lr[i]);
+    c->decay[i] = (float)(1.0 - lr * (double)a.wd[i]);
+    c->rate[i] = (float)(lr / (1.0 - p1));
+  }
+  if (threadIdx.x != 0) return;
+  if (a.norm != nullptr) *a.norm = (float)norm;
+  c->sumsq = total;
+  c->skip = skip ? 1u : 0u;
+  if (skip) {
+    c->skipped += 1;
+    return;
+  }
+  double coef = 1.0;
+  if (a.max_norm > 0.0f && !(norm <= (double)a.max_norm)) coef = (double)a.max_norm / norm;
+  c->gscale = (float)((double)a.grad_scale * coef);
+  c->rbc2 = (float)(1.0 / sqrt(1.0 - p2));
+  c->steps = t;
+  c->p1 = p1;
+  c->p2 = p2;
+  // two keys for the step's random bits; the multipliers are digits of the
+  // square roots of 2, 3 and 5
+  uint64_t z = a.seed * 0x6A09E667F3BCC909ull + (uint64_t)t * 0xBB67AE8584CAA73Bull;
+  z = mix64(z, 0x3C6EF372FE94F82Bull);
+  z = mix64(z, 0x6A09E667F3BCC909ull);
+  z ^= z >> 32;
+  c->k0 = (uint32_t)z;
+  c->k1 = (uint32_t)(z >> 32);
+}
+
+__global__ void set_steps_kernel(Control* c, int64_t steps, double p1, double p2) {
+  c->steps = steps;
+  c->skipped = 0;
+  c->p1 = p1;
+  c->p2 = p2;
+}
+
+__global__ void __launch_bounds__(kBlock)
+    fill_kernel(uint32_t* __restrict__ dst, uint32_t word, uint64_t words) {
+  const uint64_t stride = (uint64_t)gridDim.x * kBlock;
+  for (uint64_t k = (uint64_t)blockIdx.x * kBlock + threadIdx.x; k < words; k += stride)
+    dst[k] = word;
+}
+
+__global__ void __launch_bounds__(kBlock)
+    master_kernel(StepPtrs ptrs, State s, uint32_t t0, int64_t c0) {
+  const ChunkRec rec = s.recs[c0 + blockIdx.x];
+  const bf16* p = (const bf16*)ptrs.p[rec.tensor - t0] + (int64_t)rec.row * kRowElems;
+  float* dst = s.master + (int64_t)rec.state_row * kRowElems;
+  for (int k = threadIdx.x; k < (int)rec.count; k += kBlock) dst[k] = widen(p[k]);
+}
+
+// ------------------------------------------------------- state in and out --
+// Eight elements a thread where offset and dst allow 16-byte accesses, one
+// otherwise (`wide` says which).
+template <int BITS, int FIELD>
+__device__ __forceinline__ float state_value(const State& s, int64_t i) {
+  if constexpr (FIELD == OB_ADAMW_MASTER) {
+    return s.master[i];
+  } else if constexpr (BITS == 32) {
+    return ((const float*)(FIELD == OB_ADAMW_M ? s.m : s.v))[i];
+  } else if constexpr (FIELD == OB_ADAMW_M) {
+    return decode_m(((const uint8_t*)s.m)[i], s.m_exp[i / kScaleElems]).x;
+  } else {
+    return decode_v(((const uint8_t*)s.v)[i], s.v_exp[i / kScaleElems]).x;
+  }
+}
+
+template <int BITS, int FIELD, bool BF16>
+__global__ void __launch_bounds__(kBlock)
+    get_kernel(State s, int64_t offset, int64_t count, int wide, void* __restrict__ dst) {
+  const int64_t stride = (int64_t)gridDim.x * kBlock;
+  const int64_t first = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+  int64_t done = 0;
+  if (wide) {
+    for (int64_t k = first; k < count / 8; k += stride) {
+      const int64_t i = offset + 8 * k;
+      f32x4 a, b;
+      if constexpr (FIELD == OB_ADAMW_MASTER || BITS == 32) {
+        const float* src = FIELD == OB_ADAMW_MASTER ? s.master
+                                                    : (const float*)(FIELD == OB_ADAMW_M ? s.m : s.v);
+        a = load4(src + i);
+        b = load4(src + i + 4);
+      } else {
+        const u32x2 c = ld_stream((const u32x2*)((const uint8_t*)(FIELD == OB_ADAMW_M ? s.m : s.v) + i));
+        const uint32_t e = (FIELD == OB_ADAMW_M ? s.m_exp : s.v_exp)[i / kScaleElems];
+        a = FIELD == OB_ADAMW_M ? decode_m(c.x, e) : decode_v(c.x, e);
+        b = FIELD == OB_ADAMW_M ? decode_m(c.y, e) : decode_v(c.y, e);
+      }
+      if constexpr (BF16) {
+        st_stream((u32x4*)dst + k, u32x4{pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
+                                         pack_bf16(b.x, b.y), pack_bf16(b.z, b.w)});
+      } else {
+        st_stream((f32x4*)dst + 2 * k, a);
+        st_stream((f32x4*)dst + 2 * k + 1, b);
+      }
+    }
+    done = count / 8 * 8;
+  }
+  for (int64_t k = done + first; k < count; k += stride) {
+    const float v = state_value<BITS, FIELD>(s, offset + k);
+    if constexpr (BF16)
+      ((uint16_t*)dst)[k] = (uint16_t)pack_bf16(v, 0.0f);
+    else
+      ((float*)dst)[k] = v;
+  }
+}
+
+// Whole groups of 256, one per wave and round, from fp32.
+template <int FIELD>
+__global__ void __launch_bounds__(kBlock)
+    set_codes_kernel(State s, int64_t group0, int64_t groups, const float* __restrict__ src) {
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = threadIdx.x & 63;
+  for (int64_t i = (int64_t)blockIdx.x * (kBlock / 64) + wave; i < groups;
+       i += (int64_t)gridDim.x * (kBlock / 64)) {
+    f32x4 x = load_some(src + i * kScaleElems + lane * 4, 4);
+    uint32_t e, c;
+    if constexpr (FIELD == OB_ADAMW_M) {
+      c = encode_m(x, &e);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = x[k] <= 0.0f ? 0.0f : x[k];  // NaN stays
+      c = encode_v(x, &e, [](int) { return 1u << 19; });
+    }
+    const int64_t at = group0 + i;
+    ((uint32_t*)(FIELD == OB_ADAMW_M ? s.m : s.v))[at * 64 + lane] = c;
+    if (lane == 0) (FIELD == OB_ADAMW_M ? s.m_exp : s.v_exp)[at] = (uint8_t)e;
+  }
+}
+
+__global__ void __launch_bounds__(kBlock)
+    set_f32_kernel(float* __restrict__ dst, int64_t count, const float* __restrict__ src,
+                   int non_negative) {
+  const int64_t stride = (int64_t)gridDim.x * kBlock;
+  for (int64_t k = (int64_t)blockIdx.x * kBlock + threadIdx.x; k < count; k += stride) {
+    const float x = src[k];
+    dst[k] = non_negative && x <= 0.0f ? 0.0f : x;
+  }
+}
+
+int grid_for(int64_t threads) {
+  const int64_t blocks = (threads + kBlock - 1) / kBlock;
+  return (int)(blocks < 1 ? 1 : (blocks > 8192 ? 8192 : blocks));
+}
+
+template <typename PT, typename GT, int BITS>
+hipError_t step_of(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
+                   hipStream_t stream) {
+  if constexpr (sizeof(PT) == 2) {
+    if (s.has_master)
+      step_kernel<PT, GT, BITS, true, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+    else if (s.stochastic)
+      step_kernel<PT, GT, BITS, false, true><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+    else
+      step_kernel<PT, GT, BITS, false, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+  } else {
+    step_kernel<PT, GT, BITS, false, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+  }
+  return hipGetLastError();
+}
+
+template <int BITS, int FIELD>
+hipError_t get_of(const State& s, int64_t offset, int64_t count, bool bf16_out, void* dst,
+                  hipStream_t stream) {
+  const int wide = offset % 8 == 0 && (uintptr_t)dst % 16 == 0;
+  const int grid = grid_for(wide ? count / 8 + 8 : count);
+  if (bf16_out)
+    get_kernel<BITS, FIELD, true><<<grid, kBlock, 0, stream>>>(s, offset, count, wide, dst);
+  else
+    get_kernel<BITS, FIELD, false><<<grid, kBlock, 0, stream>>>(s, offset, count, wide, dst);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
+                       hipStream_t stream) {
+  if (s.state_bits == 32) {
+    if (s.param_bf16)
+      return s.grad_bf16 ? step_of<bf16, bf16, 32>(s, ptrs, t0, c0, n, stream)
+                         : step_of<bf16, float, 32>(s, ptrs, t0, c0, n, stream);
+    return s.grad_bf16 ? step_of<float, bf16, 32>(s, ptrs, t0, c0, n, stream)
+                       : step_of<float, float, 32>(s, ptrs, t0, c0, n, stream);
+  }
+  if (s.param_bf16)
+    return s.grad_bf16 ? step_of<bf16, bf16, 8>(s, ptrs, t0, c0, n, stream)
+                       : step_of<bf16, float, 8>(s, ptrs, t0, c0, n, stream);
+  return s.grad_bf16 ? step_of<float, bf16, 8>(s, ptrs, t0, c0, n, stream)
+                     : step_of<float, float, 8>(s, ptrs, t0, c0, n, stream);
+}
+
+hipError_t launch_norm(const State& s, const NormPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
+                       int64_t at, hipStream_t stream) {
+  const unsigned grid = (unsigned)norm_partials(n);
+  if (s.grad_bf16)
+    norm_kernel<bf16><<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, s.partials + at);
+  else
+    norm_kernel<float><<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, s.partials + at);
+  return hipGetLastError();
+}
+
+hipError_t launch_control(const State& s, const ControlArgs& a, hipStream_t stream) {
+  control_kernel<<<1, kBlock, 0, stream>>>(s.control, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_finish(const State& s, int64_t n_partials, float grad_scale, double* sumsq,
+                              float* norm, hipStream_t stream) {
+  norm_finish_kernel<<<1, kBlock, 0, stream>>>(s.partials, n_partials, grad_scale, sumsq, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_set_steps(const State& s, int64_t steps, double p1, double p2,
+                            hipStream_t stream) {
+  set_steps_kernel<<<1, 1, 0, stream>>>(s.control, steps, p1, p2);
+  return hipGetLastError();
+}
+
+hipError_t launch_fill(void* dst, uint32_t word, uint64_t words, hipStream_t stream) {
+  if (words == 0) return hipSuccess;
+  fill_kernel<<<grid_for((int64_t)words), kBlock, 0, stream>>>((uint32_t*)dst, word, words);
+  return hipGetLastError();
+}
+
+hipError_t launch_master(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
+                         hipStream_t stream) {
+  master_kernel<<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+  return hipGetLastError();
+}
+
+hipError_t launch_get(const State& s, int field, int64_t offset, int64_t count, bool bf16_out,
+                      void* dst, hipStream_t stream) {
+  if (field == OB_ADAMW_MASTER)
+    return get_of<32, OB_ADAMW_MASTER>(s, offset, count, bf16_out, dst, stream);
+  if (s.state_bits == 32)
+    return field == OB_ADAMW_M ? get_of<32, OB_ADAMW_M>(s, offset, count, bf16_out, dst, stream)
+                               : get_of<32, OB_ADAMW_V>(s, offset, count, bf16_out, dst, stream);
+  return field == OB_ADAMW_M ? get_of<8, OB_ADAMW_M>(s, offset, count, bf16_out, dst, stream)
+                             : get_of<8, OB_ADAMW_V>(s, offset, count, bf16_out, dst, stream);
+}
+
+hipError_t launch_set(const State& s, int field, int64_t offset, int64_t count, const float* src,
+                      hipStream_t stream) {
+  if (field != OB_ADAMW_MASTER && s.state_bits == 8) {
+    const int64_t groups = count / kScaleElems;
+    const int grid = grid_for(groups * 64);
+    if (field == OB_ADAMW_M)
+      set_codes_kernel<OB_ADAMW_M><<<grid, kBlock, 0, stream>>>(s, offset / kScaleElems, groups,
+                                                                src);
+    else
+      set_codes_kernel<OB_ADAMW_V><<<grid, kBlock, 0, stream>>>(s, offset / kScaleElems, groups,
+                                                                src);
+    return hipGetLastError();
+  }
+  float* dst = field == OB_ADAMW_MASTER ? s.master
+                                        : (float*)(field == OB_ADAMW_M ? s.m : s.v);
+  set_f32_kernel<<<grid_for(count), kBlock, 0, stream>>>(dst + offset, count, src,
+                                                         field == OB_ADAMW_V);
+  return hipGetLastError();
+}
+
+}  // namespace adamw
+}  // namespace ob

@@ -255,7 +255,34 @@ class GradBatch:
         return iter(self.tensors)
 
 
-class OneBitAdam:
+class OnStream:
+    """What has a `device` and a library `stream` of its own."""
+
+    def _separate(self):
+        return torch.cuda.current_stream(self.device) != self.stream
+
+    def _order_after_caller(self, *tensors):
+        if self._separate():
+            self.stream.wait_stream(torch.cuda.current_stream(self.device))
+            for t in tensors:
+                t.record_stream(self.stream)
+
+    def _ordered(self, tensors, fn, *args):
+        """fn(*args) on the library's stream, ordered after the caller's
+        current stream and the caller's stream after it (tensors recorded on
+        the library's stream when the two differ); one stream query."""
+        cur = torch.cuda.current_stream(self.device)
+        if cur == self.stream:
+            fn(*args)
+            return
+        self.stream.wait_stream(cur)
+        for t in tensors:
+            t.record_stream(self.stream)
+        fn(*args)
+        cur.wait_stream(self.stream)
+
+
+class OneBitAdam(OnStream):
     """A handle plus the torch-allocated workspace it lives in."""
 
     def __init__(self, d, n_workers, grad_dtype=OB_GRAD_F32, beta1=0.9, beta2=0.999, eps=1e-8,
@@ -295,29 +322,6 @@ class OneBitAdam:
             x0p = x0.data_ptr()
         self.h = ob_adam_init(self.cfg, self.workspace.data_ptr(), self.ws_bytes, x0p,
                               self.stream.cuda_stream)
-
-    def _separate(self):
-        return torch.cuda.current_stream(self.device) != self.stream
-
-    def _order_after_caller(self, *tensors):
-        if self._separate():
-            self.stream.wait_stream(torch.cuda.current_stream(self.device))
-            for t in tensors:
-                t.record_stream(self.stream)
-
-    def _ordered(self, tensors, fn, *args):
-        """fn(*args) on the library's stream, ordered after the caller's
-        current stream and the caller's stream after it (tensors recorded on
-        the library's stream when the two differ); one stream query."""
-        cur = torch.cuda.current_stream(self.device)
-        if cur == self.stream:
-            fn(*args)
-            return
-        self.stream.wait_stream(cur)
-        for t in tensors:
-            t.record_stream(self.stream)
-        fn(*args)
-        cur.wait_stream(self.stream)
 
     def _grad_ptrs(self, grads, count=None):
         """Device pointers of `count` (default n) checked gradient tensors."""

@@ -1,0 +1,310 @@
+"""The host side of ob_adamw without a GPU: the interface's exports and
+header, the workspace's layout, the list of chunks that the kernels index by
+(every access they make inside its buffer), the launch spans, and every
+refusal that comes before a HIP call.  Also the 64-bit form the GPU tests use,
+against torch's own AdamW in float64."""
+import ctypes
+import math
+import os
+import random
+import re
+import subprocess
+
+import numpy as np
+import pytest
+
+import adamw_common as A
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PKG = os.path.join(ROOT, "communication_compressed_distributed_02_amd")
+LIB = os.path.join(PKG, "libob_adam.so")
+ARG, SHAPE, PHASE, WORKSPACE = 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module")
+def oa():
+    if not os.path.exists(LIB):
+        pytest.skip("libob_adam.so not built")
+    from communication_compressed_distributed_02_amd import ob_adamw
+    return ob_adamw
+
+
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("shim") / "libshim.so")
+    subprocess.check_call(
+        ["g++", "-std=c++17", "-O1", "-g", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC",
+         "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-static-libubsan",
+         "-I", os.path.join(ROOT, "include"), "-I", os.path.join(PKG, "csrc"),
+         os.path.join(ROOT, "tests", "c_abi", "adamw_plan_shim.cpp"), "-o", so])
+    L = ctypes.CDLL(so)
+    L.shim_length.restype = L.shim_recs.restype = L.shim_spans.restype = ctypes.c_int64
+    return L
+
+
+def i64(values):
+    return (ctypes.c_int64 * max(1, len(values)))(*values)
+
+
+REC = np.dtype([("tensor", "<u4"), ("row", "<u4"), ("state_row", "<u4"), ("count", "<u2"),
+                ("group", "<u2")])
+
+
+def recs_of(shim, cfg, sizes, groups=None):
+    want = sum(-(-n // 4096) for n in sizes)
+    out, parts = np.zeros(want + 1, REC), ctypes.c_int64(0)
+    g = None if groups is None else (ctypes.c_int32 * len(groups))(*groups)
+    n = shim.shim_recs(ctypes.byref(cfg), i64(sizes), g, out.ctypes.data_as(ctypes.c_void_p),
+                       ctypes.c_int64(out.size), ctypes.byref(parts))
+    assert n == want
+    return out[:n], parts.value
+
+
+def test_header_and_exports(oa):
+    src = open(os.path.join(ROOT, "include", "ob_adamw.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    declared = sorted(set(re.findall(r"\b(ob_adamw_\w+)\s*\(", src)))
+    assert sorted(oa.EXPORTED) == declared
+    out = subprocess.check_output(["nm", "-D", "--defined-only", LIB], text=True)
+    exported = {line.split()[-1] for line in out.splitlines() if " T " in line}
+    assert set(declared) <= exported
+    prog = '#include "ob_adamw.h"\nint main(void) { ob_adamw_config c = {0}; (void)c; return 0; }\n'
+    subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Wextra", "-Werror", "-fsyntax-only",
+                    "-I", os.path.join(ROOT, "include"), "-x", "c", "-"], input=prog, text=True,
+                   check=True)
+
+
+def size_lists():
+    r = random.Random(1)
+    yield [1]
+    yield [0]
+    yield [0, 5, 0, 4096, 4097, 0]
+    yield [1023, 1024, 1025, 3 * 4096]
+    yield [r.choice([0, 1, 7, 255, 256, 5000, 20000]) for _ in range(481)]
+    yield [r.randrange(9000) for _ in range(1000)]
+
+
+def test_chunks_cover_every_element_once_and_stay_inside(shim, oa):
+    """The kernels' accesses, from the records: wave w of a chunk touches
+    min(1024, count - 1024w) elements of the tensor and a whole row of 1024
+    of every state array."""
+    for sizes in size_lists():
+        cfg = oa.make_config(len(sizes), 3)
+        offsets = i64([0] * len(sizes))
+        length = shim.shim_length(ctypes.byref(cfg), i64(sizes), offsets)
+        groups = [i % 3 for i in range(len(sizes))]
+        recs, _ = recs_of(shim, cfg, sizes, groups)
+        seen = [np.zeros(n, np.int8) for n in sizes]
+        state = np.zeros(length // 1024, np.int8)
+        for rec in recs:
+            i, count = int(rec["tensor"]), int(rec["count"])
+            assert 1 <= count <= 4096 and rec["group"] == groups[i]
+            begin = int(rec["row"]) * 1024
+            assert begin % 4096 == 0 and begin + count <= sizes[i]
+            seen[i][begin:begin + count] += 1
+            assert int(rec["state_row"]) * 1024 == offsets[i] + begin
+            rows = -(-count // 1024)
+            assert int(rec["state_row"]) + rows <= length // 1024
+            state[int(rec["state_row"]):int(rec["state_row"]) + rows] += 1
+        assert all((s == 1).all() for s in seen) and (state == 1).all()
+
+
+def test_spans_hold_their_tensors_and_partials(shim, oa):
+    for sizes in size_lists():
+        cfg = oa.make_config(len(sizes))
+        recs, partials = recs_of(shim, cfg, sizes)
+        for which, per in ((0, 240), (1, 480)):
+            out = i64([0] * 4 * (len(sizes) + 1))
+            n = shim.shim_spans(ctypes.byref(cfg), i64(sizes), which, out,
+                                ctypes.c_int64(len(sizes) + 1))
+            at, total = 0, 0
+            for k in range(n):
+                t0, count, c0, chunks = out[4 * k:4 * k + 4]
+                assert 1 <= count <= per and chunks > 0 and c0 == at
+                ids = recs["tensor"][c0:c0 + chunks]
+                assert ids.min() >= t0 and ids.max() < t0 + count
+                at += chunks
+                total += min(chunks, 2048)
+            assert at == len(recs)
+            if which:
+                assert total == partials
+
+
+def test_buffers_of_the_workspace_do_not_overlap(shim, oa):
+    for sizes in size_lists():
+        for kw in ({}, {"state_bits": 8}, {"state_bits": 0},
+                   {"param_dtype": 1, "master": True}, {"param_dtype": 1, "state_bits": 8,
+                                                        "master": True}):
+            cfg = oa.make_config(len(sizes), **kw)
+            out = (ctypes.c_uint64 * 17)()
+            shim.shim_places(ctypes.byref(cfg), i64(sizes), ctypes.c_uint64(1000), out)
+            n = sum(-(-s // 1024) * 1024 for s in sizes)
+            chunks = sum(-(-s // 4096) for s in sizes)
+            bits = cfg.state_bits
+            _, partials = recs_of(shim, cfg, sizes)
+            need = [1000, 16 * chunks, 8 * partials, n * bits // 8, n * bits // 8,
+                    n // 256 if bits == 8 else 0, n // 256 if bits == 8 else 0,
+                    4 * n if cfg.master else 0]
+            at = 0
+            for k in range(8):
+                assert out[k] == at and out[9 + k] >= out[k] + need[k] and out[9 + k] % 256 == 0
+                at = out[9 + k] + 256
+            assert out[8] == at
+
+
+def test_layout_and_configurations(oa):
+    """ob_adamw_layout through the library, and every configuration refused."""
+    from communication_compressed_distributed_02_amd.ob_adam import ObAdamError
+
+    def status(cfg, sizes):
+        with pytest.raises(ObAdamError) as e:
+            oa.ob_adamw_layout(cfg, sizes)
+        return e.value.status
+
+    offsets, length, need = oa.ob_adamw_layout(oa.make_config(3), [5, 0, 5000])
+    assert offsets == [0, 1024, 1024] and length == 1024 + 5 * 1024 and need > 8 * length
+    big = (1 << 40)
+    assert oa.ob_adamw_layout(oa.make_config(1), [big])[1] == big
+    for sizes in ([-1], [big + 1], [big, 1]):
+        assert status(oa.make_config(len(sizes)), sizes) == SHAPE
+    assert status(oa.make_config(0), []) == SHAPE
+    for kw in ({"n_groups": 0}, {"n_groups": 33}, {"param_dtype": 2}, {"grad_dtype": -1},
+               {"state_bits": 16}, {"beta1": 1.0}, {"beta2": -0.1}, {"beta1": math.nan},
+               {"eps": 0.0}, {"eps": math.inf}, {"master": True}, {"stochastic": True},
+               {"param_dtype": 1, "master": True, "stochastic": True},
+               {"param_dtype": 1, "master": True, "state_bits": 0}):
+        assert status(oa.make_config(1, **kw), [10]) == ARG, kw
+
+
+def test_refusals_before_any_device_call(oa):
+    from communication_compressed_distributed_02_amd.ob_adam import ObAdamError
+
+    def status(fn, *args):
+        with pytest.raises(ObAdamError) as e:
+            fn(*args)
+        return e.value.status
+
+    cfg = oa.make_config(1, 2)
+    _, _, need = oa.ob_adamw_layout(cfg, [100])
+    for ptr, size in ((None, need), (256, need - 1), (257, need)):
+        assert status(oa.ob_adamw_init, cfg, [100], None, ptr, size, None, None) == WORKSPACE
+        assert status(oa.ob_adamw_attach, cfg, [100], None, ptr, size, None) == WORKSPACE
+    assert status(oa.ob_adamw_init, cfg, [100], [2], 256, need, None, None) == ARG
+    assert status(oa.ob_adamw_init, cfg, [100], [-1], 256, need, None, None) == ARG
+    for fn, args in ((oa.ob_adamw_get_steps, ()), (oa.ob_adamw_set_steps, (1,)),
+                     (oa.ob_adamw_check_guards, ()), (oa.ob_adamw_state, (0,)),
+                     (oa.ob_adamw_get_state, (0, 0, 1, 0, None)),
+                     (oa.ob_adamw_set_state, (0, 0, 1, None)),
+                     (oa.ob_adamw_grad_norm, (None, 1.0, None, None)),
+                     (oa.ob_adamw_step, (None, None, None)), (oa.ob_adamw_destroy, ())):
+        assert status(fn, None, *args) == ARG, fn.__name__
+    import torch
+    with pytest.raises(ValueError):
+        oa.AdamW([torch.zeros(8)])
+    with pytest.raises(ValueError):
+        oa.AdamW([])
+
+
+def test_pointer_check(shim, oa):
+    """Overlaps of what is written, alignment and missing pointers; addresses
+    are never followed."""
+    P = ctypes.c_void_p
+
+    def check(params, grads, sizes=(100, 50), base=1 << 20, ws=4096, times=1, **kw):
+        cfg = oa.make_config(len(sizes), **kw)
+        return shim.shim_ptrs(ctypes.byref(cfg), i64(sizes), (P * len(sizes))(*params),
+                              (P * len(sizes))(*grads), P(base), ctypes.c_uint64(ws), times)
+
+    assert check([1000, 2000], [4000, 5000]) == 0
+    assert check([1000, 2000], [4000, 5000], times=3) == 0
+    assert check([1000, 1400], [4000, 5000]) == 0         # one ends where the next begins
+    assert check([1000, 1396], [4000, 5000]) == ARG       # 4 bytes of overlap
+    assert check([1000, 1396], [4000, 5000], times=2) == ARG
+    assert check([1396, 1000], [4000, 5000]) == 0
+    assert check([1000, 1000], [4000, 5000]) == ARG       # the same tensor twice
+    assert check([1000, 2000], [4000, 4000]) == 0         # gradients may be shared
+    assert check([1000, 2000], [4000, 4200]) == 0
+    assert check([1000, 2000], [1000, 5000]) == ARG       # a gradient in a parameter
+    assert check([1000, 2000], [2100, 5000]) == ARG
+    assert check([1000, 2000], [1800, 5000]) == ARG       # it ends in the second parameter
+    assert check([1000, 2000], [4000, 2196]) == ARG
+    assert check([1000, 1000], [4000, None]) == 0         # no gradient: not touched
+    assert check([1000, None], [4000, None]) == 0
+    assert check([1000, None], [4000, 5000]) == ARG
+    assert check([1002, 2000], [4000, 5000]) == ARG
+    assert check([1000, 2000], [4002, 5000]) == ARG
+    assert check([1002, 2000], [4002, 5000], param_dtype=1, grad_dtype=1) == 0
+    assert check([1001, 2000], [4002, 5000], param_dtype=1, grad_dtype=1) == ARG
+    assert check([1000, None], [4000, None], sizes=(100, 0)) == 0
+    assert check([(1 << 20) + 4092, 2000], [4000, 5000]) == ARG   # in the workspace
+    assert check([(1 << 20) + 4096, 2000], [4000, 5000]) == 0
+    assert check([1000, 2000], [(1 << 20) - 396, 5000]) == ARG    # the gradient reaches into it
+
+
+def test_step_arguments_and_ranges(shim, oa):
+    one = (ctypes.c_float * 2)(1e-3, 1e-3)
+    bad = (ctypes.c_float * 2)(1e-3, math.nan)
+    fp = ctypes.POINTER(ctypes.c_float)
+
+    def step(bits=32, lr=one, wd=None, **kw):
+        cfg = oa.make_config(1, 2, state_bits=bits)
+        a = oa.ob_adamw_step_args()
+        a.lr = ctypes.cast(lr, fp) if lr is not None else None
+        a.weight_decay = ctypes.cast(wd, fp) if wd is not None else None
+        a.grad_scale = 1.0
+        for k, v in kw.items():
+            setattr(a, k, v)
+        return shim.shim_step(ctypes.byref(cfg), i64([10]), ctypes.byref(a))
+
+    assert step() == 0 and step(lr=None, lr_device=64) == 0 and step(wd=one, max_norm=1.0) == 0
+    assert step(max_norm=math.inf) == 0
+    assert step(bits=0) == PHASE
+    for kw in ({"lr": None}, {"lr": bad}, {"wd": bad}, {"grad_scale": 0.0},
+               {"grad_scale": -1.0}, {"grad_scale": math.inf}, {"max_norm": -1.0},
+               {"max_norm": math.nan}, {"skip_nonfinite": 2}, {"lr_device": 2}, {"sumsq": 4},
+               {"norm": 2}):
+        assert step(**kw) == ARG, kw
+    cfg8 = oa.make_config(1, state_bits=8)
+    cfg32 = oa.make_config(1)
+
+    def rng(cfg, field, offset, count, whole):
+        return shim.shim_range(ctypes.byref(cfg), i64([2000]), field, ctypes.c_int64(offset),
+                               ctypes.c_int64(count), whole)
+
+    for cfg in (cfg8, cfg32):
+        assert rng(cfg, 0, 0, 2048, 1) == 0 and rng(cfg, 1, 1792, 256, 1) == 0
+        assert rng(cfg, 0, 3, 5, 0) == 0 and rng(cfg, 0, 2048, 0, 0) == 0
+        for offset, count in ((-1, 1), (0, -1), (0, 2049), (2049, 0), (1, 1 << 62)):
+            assert rng(cfg, 0, offset, count, 0) == ARG
+        for field in (2, 3, 4, 5, -1):
+            assert rng(cfg, field, 0, 1, 0) == ARG
+    assert rng(cfg8, 0, 1, 256, 1) == ARG and rng(cfg8, 1, 0, 255, 1) == ARG
+    assert rng(cfg32, 0, 1, 255, 1) == 0
+
+
+def test_formulas_agree_with_torch_in_float64():
+    import torch
+    r = np.random.RandomState(0)
+    x = r.randn(500)
+    p = torch.nn.Parameter(torch.from_numpy(x.copy()))
+    lr, wd = float(np.float32(1e-2)), float(np.float32(0.1))
+    opt = torch.optim.AdamW([p], lr=lr, weight_decay=wd, eps=float(A.EPS),
+                            betas=(float(A.B1), float(A.B2)))
+    m, v = np.zeros(500), np.zeros(500)
+    for t in range(1, 8):
+        g = r.randn(500)
+        p.grad = torch.from_numpy(g.copy())
+        opt.step()
+        (x, m, v), _ = A.step64(x, m, v, g, t, 1e-2, 0.1)
+        assert np.allclose(p.detach().numpy(), x, rtol=1e-12, atol=1e-13)
+
+
+def test_fp32_form_is_within_its_bounds():
+    r = np.random.RandomState(1)
+    for t in (1, 2, 50, 5000):
+        x, m, v, g = (r.randn(4000) * s for s in (0.1, 1e-3, 1e-3, 1e-2))
+        x, m, v, g = (a.astype(np.float32) for a in (x, m, v * v, g))
+        (x64, m64, v64), (dx, dm, dv) = A.step64(x, m, v, g, t, 1e-3, 0.01)
+        x32, m32, v32 = A.step32(x, m, v, g, t, 1e-3, 0.01)
+        for a, b, d in ((x32, x64, dx), (m32, m64, dm), (v32, v64, dv)):
+            assert np.all(np.abs(a - b) <= d)
