@@ -60,8 +60,9 @@ struct State {
 hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        hipStream_t stream);
 // The same for the norm, leaving norm_partials(n) values from partials[at].
+// keep: a step follows (its first gradients are left in the caches).
 hipError_t launch_norm(const State& s, const NormPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
-                       int64_t at, hipStream_t stream);
+                       int64_t at, bool keep, hipStream_t stream);
 // Folds the partials (or reads sumsq) and advances the step.
 hipError_t launch_control(const State& s, const ControlArgs& a, hipStream_t stream);
 // Folds the partials into the caller's sumsq and norm.

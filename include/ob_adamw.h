@@ -133,10 +133,9 @@ typedef struct {
 } ob_adamw_step_args;
 
 /* One step.  params, grads: host arrays of n_tensors device pointers,
- * contiguous, aligned to their element size (wide accesses are used where a
- * tensor's pointers are aligned to 4 elements).  A tensor without a
- * gradient (NULL) is left as it is, state included, and its parameter pointer
- * may be NULL.  Parameters may overlap neither each other nor a gradient nor
+ * contiguous, aligned to their element size.  A tensor without a gradient
+ * (NULL) is left as it is, state included, and its parameter pointer may be
+ * NULL.  Parameters may overlap neither each other nor a gradient nor
  * the workspace (OB_ERR_ARG); gradients may overlap each other.  The step
  * count is kept on the device and the call enqueues kernel launches only, so
  * a captured step may be replayed: each replay is one more step on the
