@@ -315,6 +315,18 @@ ob_status ob_adamw_step(ob_adamw_t h, const void* const* params, const void* con
     c.partials = h->st.partials;
     c.n_partials = h->plan.n_partials;
   }
+  const std::vector<aw::ChunkRec>& few = h->plan.small;
+  if (e == hipSuccess && !few.empty()) {
+    aw::SmallStep k;
+    k.s = h->st;
+    k.a = c;
+    for (size_t i = 0; i < few.size(); ++i) {
+      const aw::ChunkRec& r = few[i];
+      k.rec[i] = {grads[r.tensor], const_cast<void*>(params[r.tensor]), r.row, r.state_row,
+                  r.count, r.group};
+    }
+    return fail(h, aw::launch_small(k, (int64_t)few.size(), h->stream));
+  }
   if (e == hipSuccess) e = aw::launch_control(h->st, c, h->stream);
   for (size_t i = 0; i < h->plan.step_spans.size() && e == hipSuccess; ++i) {
     const aw::Span& s = h->plan.step_spans[i];

@@ -21,13 +21,13 @@ struct NormPtrs {
   const void* g[kPtrsPerNorm];
 };
 
-// The step's scalars and the step count, on the device.
+// The step count and the scalars of the step that follows, on the device.
 struct Control {
   int64_t steps, skipped;
   double p1, p2;             // b1^steps, b2^steps
-  double sumsq;              // S of the last norm that the plan computed itself
   float gscale, rbc2;
-  uint32_t skip, k0, k1, pad;
+  uint32_t skip, k0, k1;
+  uint32_t ticket;           // waves of a small step that have read the above
   float decay[kMaxGroups], rate[kMaxGroups];
 };
 
@@ -56,6 +56,23 @@ struct State {
   int32_t param_bf16, grad_bf16, state_bits, has_master, stochastic;
 };
 
+// A small step's work, in the arguments of its one launch: each chunk with
+// its own pointers.
+struct SmallRec {
+  const void* g;
+  void* p;
+  uint32_t row, state_row;
+  uint16_t count, group;
+};
+struct SmallStep {
+  State s;
+  ControlArgs a;
+  SmallRec rec[kSmallChunks];
+};
+static_assert(sizeof(SmallStep) <= 4096, "kernel arguments");
+
+// A step of n <= kSmallChunks chunks: control and update in one launch.
+hipError_t launch_small(const SmallStep& p, int64_t n, hipStream_t stream);
 // Chunks [c0, c0 + n) of tensors t0, t0 + 1, ... whose pointers `ptrs` holds.
 hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        hipStream_t stream);

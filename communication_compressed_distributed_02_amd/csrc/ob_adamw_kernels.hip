@@ -32,6 +32,11 @@ struct bf16 {
   uint16_t bits;
 };
 
+// Index of this wavefront in its block, as a wave-uniform (scalar) value.
+__device__ __forceinline__ int wave_in_block() {
+  return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(bf16 x) { return __uint_as_float((uint32_t)x.bits << 16); }
 
@@ -314,7 +319,9 @@ __device__ __forceinline__ void store_param(bf16* p, u32x2 w, int n) {
 
 // A step's scalars, the same for every element of a row.
 struct Scalars {
-  float gs, decay, rate, rbc2, eps, b1, ob1, b2, ob2;
+  float gs, decay, rate, rbc2;
+  uint32_t key0, key1;
+  bool skip;
 };
 
 // The four random words of this lane's quad of group u.
@@ -359,10 +366,10 @@ __device__ __forceinline__ uint32_t special_codes(uint32_t c) {
 }
 
 // One row of 1024 elements of one tensor.  WHOLE: all of them are the tensor's.
-template <typename PT, typename GT, int BITS, bool MASTER, bool SR, bool WHOLE>
+// scalars() is called when the row's loads are under way.
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR, bool WHOLE, typename F>
 __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int64_t srow,
-                                         int left, const Scalars& c, uint32_t key0,
-                                         uint32_t key1) {
+                                         int left, F scalars) {
   const int lane = threadIdx.x & 63;
   const int at = lane * 4;
   float* master = s.master + srow * kRowElems + at;
@@ -394,8 +401,12 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
     me = *(const uint32_t*)(s.m_exp + srow * kGroups);
     ve = *(const uint32_t*)(s.v_exp + srow * kGroups);
   }
+  const Scalars c = scalars();
+  if (c.skip) return;
+  const float b1 = s.beta1, ob1 = 1.0f - b1, b2 = s.beta2, ob2 = 1.0f - b2;
   const uint64_t quad0 = (uint64_t)srow * (kRowElems / 4);
-  const bool plain_scalars = c.eps >= 0x1p-30f && c.b2 >= 0x1p-10f;
+  const uint32_t key0 = high_key(quad0, c.key0), key1 = c.key1;
+  const bool plain_scalars = s.eps >= 0x1p-30f && b2 >= 0x1p-10f;
   uint32_t new_me = 0, new_ve = 0;
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) {
@@ -412,9 +423,9 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
       v = vv[u];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m[k] = moment1(m[k], gv[k], c.b1, c.ob1);
-        v[k] = moment2(v[k], gv[k], c.b2, c.ob2);
-        x[k] = updated(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, c.eps);
+        m[k] = moment1(m[k], gv[k], b1, ob1);
+        v[k] = moment2(v[k], gv[k], b2, ob2);
+        x[k] = updated(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, s.eps);
       }
       if constexpr (!WHOLE) clear_behind(n, m, v, x);
       put<SR, true, WHOLE>(p + o, x, n, w);
@@ -427,7 +438,7 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
       bool plain = plain_scalars && em >= 16u && __ballot(special_codes(vc[u])) == 0;
       if (plain) {
         // b1 * (code * 2^k) rounds as (b1 * 2^k) * code does
-        const float bs = c.b1 * __uint_as_float((em - 7u) << 23);
+        const float bs = b1 * __uint_as_float((em - 7u) << 23);
         const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[u], false);
         const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[u], true);
         m = f32x4{bs * lo.x, bs * lo.y, bs * hi.x, bs * hi.y};
@@ -436,14 +447,14 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
         for (int k = 0; k < 4; ++k)
           v[k] = __uint_as_float((((vc[u] >> (8 * k)) & 255u) + low) << 20);
       } else {
-        m = decode_m(mc[u], em) * c.b1;
+        m = decode_m(mc[u], em) * b1;
         v = decode_v(vc[u], ev);
       }
       uint32_t q[4], tm = 0, tv = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        m[k] = m[k] + (c.ob1 * gv[k]);
-        v[k] = moment2(v[k], gv[k], c.b2, c.ob2);
+        m[k] = m[k] + (ob1 * gv[k]);
+        v[k] = moment2(v[k], gv[k], b2, ob2);
       }
       if constexpr (!WHOLE) {
         f32x4 unused = x;
@@ -461,7 +472,7 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
       if (plain && tm < (217u << 23) && tv < (227u << 3) && WHOLE) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          x[k] = updated_plain(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, c.eps);
+          x[k] = updated_plain(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, s.eps);
         put<SR, false, WHOLE>(p + o, x, n, w);
         e = umax(tm >> 23, (uint32_t)kMinExpM);
         new_me |= e << (8 * u);
@@ -477,7 +488,7 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          x[k] = updated(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, c.eps);
+          x[k] = updated(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, s.eps);
         if constexpr (!WHOLE) clear_behind(n, m, v, x);
         put<SR, true, WHOLE>(p + o, x, n, w);
         cm = encode_m(m, &e);
@@ -498,6 +509,20 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
   }
 }
 
+// This wave's row of a chunk: rows of one block are the chunk's four.
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR, typename F>
+__device__ __forceinline__ void step_wave(const GT* g, PT* p, const State& s, uint32_t row0,
+                                          uint32_t state_row, int wave, int left, F scalars) {
+  const int64_t row = (int64_t)row0 + wave;
+  const int64_t srow = (int64_t)state_row + wave;
+  g += row * kRowElems;
+  p += row * kRowElems;
+  if (left >= kRowElems)
+    step_row<PT, GT, BITS, MASTER, SR, true>(g, p, s, srow, left, scalars);
+  else
+    step_row<PT, GT, BITS, MASTER, SR, false>(g, p, s, srow, left, scalars);
+}
+
 template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
 __global__ void __launch_bounds__(kBlock)
     step_kernel(StepPtrs ptrs, State s, uint32_t t0, int64_t c0) {
@@ -506,21 +531,13 @@ __global__ void __launch_bounds__(kBlock)
   const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
   PT* p = (PT*)ptrs.p[rec.tensor - t0];
   if (g == nullptr || ctl->skip) return;
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = wave_in_block();
   const int left = (int)rec.count - wave * kRowElems;  // elements from this wave's row on
   if (left <= 0) return;
-  const int64_t row = (int64_t)rec.row + wave;
-  const int64_t srow = (int64_t)rec.state_row + wave;
-  g += row * kRowElems;
-  p += row * kRowElems;
-  const Scalars c = {ctl->gscale, ctl->decay[rec.group], ctl->rate[rec.group], ctl->rbc2,
-                     s.eps,       s.beta1,               1.0f - s.beta1,       s.beta2,
-                     1.0f - s.beta2};
-  const uint32_t key0 = high_key((uint64_t)srow * (kRowElems / 4), ctl->k0), key1 = ctl->k1;
-  if (left >= kRowElems)
-    step_row<PT, GT, BITS, MASTER, SR, true>(g, p, s, srow, left, c, key0, key1);
-  else
-    step_row<PT, GT, BITS, MASTER, SR, false>(g, p, s, srow, left, c, key0, key1);
+  step_wave<PT, GT, BITS, MASTER, SR>(g, p, s, rec.row, rec.state_row, wave, left, [&] {
+    return Scalars{ctl->gscale, ctl->decay[rec.group], ctl->rate[rec.group], ctl->rbc2,
+                   ctl->k0,     ctl->k1,               false};
+  });
 }
 
 // ------------------------------------------------------------------ norm --
@@ -541,32 +558,40 @@ __device__ __forceinline__ double block_sum(double acc, double* red) {
 // bfloat16 gradients: 1544 us with none kept, 1525 with 128 MB, 1506 with 240
 // MB).  A norm on its own streams everything from the first chunk on, 1 %
 // faster than backwards (6.2 GB: 936 and 945 us).
-template <typename GT>
+template <typename GT, bool KEEP>
 __global__ void __launch_bounds__(kBlock)
     norm_kernel(NormPtrs ptrs, const ChunkRec* __restrict__ recs, uint32_t t0, int64_t c0,
                 int64_t n, int64_t kept, double* __restrict__ partials) {
   __shared__ double red[kBlock / 64];
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = wave_in_block();
   const int at = (threadIdx.x & 63) * 4;
+  const auto chunk = [&](int64_t i) { return KEEP ? c0 + n - 1 - i : c0 + i; };
   double acc = 0.0;
-  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-    const int64_t c = kept > 0 ? c0 + n - 1 - i : c0 + i;
-    const ChunkRec rec = recs[c];
-    const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
-    const int left = (int)rec.count - wave * kRowElems;
-    if (g == nullptr || left <= 0) continue;
-    g += ((int64_t)rec.row + wave) * kRowElems;
+  int64_t i = blockIdx.x;
+  ChunkRec rec = recs[chunk(i)];
+  const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
+  while (i < n) {
+    const int left = g == nullptr ? 0 : (int)rec.count - wave * kRowElems;
+    const GT* p = g + ((int64_t)rec.row + wave) * kRowElems + at;
     f32x4 v[kGroups];
-    if (left >= kRowElems && c < kept) {
+    if (left >= kRowElems) {
+      if (KEEP && chunk(i) < kept) {
 #pragma unroll
-      for (int u = 0; u < kGroups; ++u) v[u] = load4_kept(g + u * kScaleElems + at);
-    } else if (left >= kRowElems) {
+        for (int u = 0; u < kGroups; ++u) v[u] = load4_kept(p + u * kScaleElems);
+      } else {
 #pragma unroll
-      for (int u = 0; u < kGroups; ++u) v[u] = load4(g + u * kScaleElems + at);
+        for (int u = 0; u < kGroups; ++u) v[u] = load4(p + u * kScaleElems);
+      }
     } else {
 #pragma unroll
-      for (int u = 0; u < kGroups; ++u) v[u] = load_some(g + u * kScaleElems + at,
+      for (int u = 0; u < kGroups; ++u) v[u] = load_some(p + u * kScaleElems,
                                                          left - u * kScaleElems - at);
+    }
+    // the next chunk's record and pointer arrive while this one's data do
+    i += gridDim.x;
+    if (i < n) {
+      rec = recs[chunk(i)];
+      g = (const GT*)ptrs.g[rec.tensor - t0];
     }
 #pragma unroll
     for (int u = 0; u < kGroups; ++u) {
@@ -603,8 +628,45 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z, uint64_t mul) {
   return z * mul;
 }
 
-// One block: S, the clipping factor, the step count and the scalars of the
-// step that follows on the stream.
+// What a step does with S: the clipping factor, the bias corrections and the
+// keys of its random bits, from the counts before it.
+struct Derived {
+  double norm, p1, p2;
+  float gscale, rbc2;
+  uint32_t k0, k1;
+  bool skip;
+};
+__device__ __forceinline__ Derived derive(const ControlArgs& a, double total, int64_t steps,
+                                          double p1, double p2) {
+  Derived d;
+  d.norm = sqrt(total) * (double)a.grad_scale;
+  d.skip = a.skip_nonfinite && !(total <= 1.7976931348623157e308);
+  d.p1 = p1 * (double)a.beta1;
+  d.p2 = p2 * (double)a.beta2;
+  double coef = 1.0;
+  if (a.max_norm > 0.0f && !(d.norm <= (double)a.max_norm)) coef = (double)a.max_norm / d.norm;
+  d.gscale = (float)((double)a.grad_scale * coef);
+  d.rbc2 = (float)(1.0 / sqrt(1.0 - d.p2));
+  // the multipliers are digits of the square roots of 2, 3 and 5
+  uint64_t z = a.seed * 0x6A09E667F3BCC909ull + (uint64_t)(steps + 1) * 0xBB67AE8584CAA73Bull;
+  z = mix64(z, 0x3C6EF372FE94F82Bull);
+  z = mix64(z, 0x6A09E667F3BCC909ull);
+  z ^= z >> 32;
+  d.k0 = (uint32_t)z;
+  d.k1 = (uint32_t)(z >> 32);
+  return d;
+}
+// The factors of group i.  A NaN rate becomes the canonical one: stochastic
+// rounding adds to bit patterns and must not carry out of a NaN.
+__device__ __forceinline__ void derive_group(const ControlArgs& a, int i, double p1, float* decay,
+                                             float* rate) {
+  double lr = (double)(a.lr_device != nullptr ? a.lr_device[i] : a.lr[i]);
+  if (lr != lr) lr = __builtin_nan("");
+  *decay = (float)(1.0 - lr * (double)a.wd[i]);
+  *rate = (float)(lr / (1.0 - p1));
+}
+
+// One block: S and the scalars of the step that follows on the stream.
 __global__ void __launch_bounds__(kBlock) control_kernel(Control* c, ControlArgs a) {
   __shared__ double red[kBlock / 64];
   double total = 0.0;
@@ -613,40 +675,91 @@ __global__ void __launch_bounds__(kBlock) control_kernel(Control* c, ControlArgs
   } else if (a.sumsq != nullptr) {
     total = *a.sumsq;
   }
-  const double norm = sqrt(total) * (double)a.grad_scale;
-  const bool skip = a.skip_nonfinite && !(total <= 1.7976931348623157e308);
-  const double p1 = c->p1 * (double)a.beta1, p2 = c->p2 * (double)a.beta2;
-  const int64_t t = c->steps + 1;
-  __syncthreads();  // every thread has read them before thread 0 writes
-  if (!skip && (int)threadIdx.x < a.n_groups) {
-    const int i = threadIdx.x;
-    const double lr = (double)(a.lr_device != nullptr ? a.lr_device[i] : a.lr[i]);
-    c->decay[i] = (float)(1.0 - lr * (double)a.wd[i]);
-    c->rate[i] = (float)(lr / (1.0 - p1));
-  }
+  const int64_t steps = c->steps;
+  const Derived d = derive(a, total, steps, c->p1, c->p2);
+  __syncthreads();  // every thread has read the counts before thread 0 writes
+  if ((int)threadIdx.x < a.n_groups)
+    derive_group(a, threadIdx.x, d.p1, &c->decay[threadIdx.x], &c->rate[threadIdx.x]);
   if (threadIdx.x != 0) return;
-  if (a.norm != nullptr) *a.norm = (float)norm;
-  c->sumsq = total;
-  c->skip = skip ? 1u : 0u;
-  if (skip) {
+  if (a.norm != nullptr) *a.norm = (float)d.norm;
+  c->skip = d.skip ? 1u : 0u;
+  if (d.skip) {
     c->skipped += 1;
     return;
   }
-  double coef = 1.0;
-  if (a.max_norm > 0.0f && !(norm <= (double)a.max_norm)) coef = (double)a.max_norm / norm;
-  c->gscale = (float)((double)a.grad_scale * coef);
-  c->rbc2 = (float)(1.0 / sqrt(1.0 - p2));
-  c->steps = t;
-  c->p1 = p1;
-  c->p2 = p2;
-  // two keys for the step's random bits; the multipliers are digits of the
-  // square roots of 2, 3 and 5
-  uint64_t z = a.seed * 0x6A09E667F3BCC909ull + (uint64_t)t * 0xBB67AE8584CAA73Bull;
-  z = mix64(z, 0x3C6EF372FE94F82Bull);
-  z = mix64(z, 0x6A09E667F3BCC909ull);
-  z ^= z >> 32;
-  c->k0 = (uint32_t)z;
-  c->k1 = (uint32_t)(z >> 32);
+  c->gscale = d.gscale;
+  c->rbc2 = d.rbc2;
+  c->k0 = d.k0;
+  c->k1 = d.k1;
+  c->steps = steps + 1;
+  c->p1 = d.p1;
+  c->p2 = d.p2;
+}
+
+// ------------------------------------------------------------ small steps --
+// Control and update in one launch, for the latency of steps over few
+// elements.  Every wave derives the scalars for itself from the counts before
+// the step while its row is being loaded, and takes a ticket once it has
+// them; the wave with the last ticket moves the counts on.  Nothing waits for
+// another wave.
+template <typename T>
+__device__ __forceinline__ T ld_shared_state(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
+__global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
+  const SmallRec rec = k.rec[blockIdx.x];
+  const ControlArgs& a = k.a;
+  Control* ctl = k.s.control;
+  const int lane = threadIdx.x & 63;
+  const int wave = wave_in_block();
+  const int left = (int)rec.count - wave * kRowElems;
+  const int64_t steps = ld_shared_state(&ctl->steps);
+  const double p1 = ld_shared_state(&ctl->p1), p2 = ld_shared_state(&ctl->p2);
+  double part = 0.0;
+  if (a.partials != nullptr) {
+    if (lane < (int)a.n_partials) part = a.partials[lane];
+  } else if (a.sumsq != nullptr && lane == 0) {
+    part = *a.sumsq;
+  }
+  const auto scalars = [&] {
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) part = part + __shfl_xor(part, o, 64);
+    const Derived d = derive(a, part, steps, p1, p2);
+    Scalars c;
+    derive_group(a, rec.group, d.p1, &c.decay, &c.rate);
+    c.gs = d.gscale;
+    c.rbc2 = d.rbc2;
+    c.key0 = d.k0;
+    c.key1 = d.k1;
+    c.skip = d.skip;
+    if (lane == 0) {
+      // What is added depends on the loaded counts, so the ticket is taken
+      // after they have arrived; steps is never negative.
+      const uint32_t one = steps >= 0 && p1 >= 0.0 && p2 >= 0.0 ? 1u : 2u;
+      const uint32_t n = __hip_atomic_fetch_add(&ctl->ticket, one, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+      if (n == gridDim.x * (kBlock / 64) - 1) {
+        ctl->ticket = 0;
+        if (a.norm != nullptr) *a.norm = (float)d.norm;
+        if (d.skip) {
+          ctl->skipped += 1;
+        } else {
+          ctl->steps = steps + 1;
+          ctl->p1 = d.p1;
+          ctl->p2 = d.p2;
+        }
+      }
+    }
+    return c;
+  };
+  if (rec.g == nullptr || left <= 0) {
+    scalars();
+    return;
+  }
+  step_wave<PT, GT, BITS, MASTER, SR>((const GT*)rec.g, (PT*)rec.p, k.s, rec.row, rec.state_row,
+                                      wave, left, scalars);
 }
 
 __global__ void set_steps_kernel(Control* c, int64_t steps, double p1, double p2) {
@@ -672,8 +785,6 @@ __global__ void __launch_bounds__(kBlock)
 }
 
 // ------------------------------------------------------- state in and out --
-// Eight elements a thread where offset and dst allow 16-byte accesses, one
-// otherwise (`wide` says which).
 template <int BITS, int FIELD>
 __device__ __forceinline__ float state_value(const State& s, int64_t i) {
   if constexpr (FIELD == OB_ADAMW_MASTER) {
@@ -687,38 +798,13 @@ __device__ __forceinline__ float state_value(const State& s, int64_t i) {
   }
 }
 
+// Any offset and alignment, an element a thread; `done` elements of dst are
+// there already.
 template <int BITS, int FIELD, bool BF16>
 __global__ void __launch_bounds__(kBlock)
-    get_kernel(State s, int64_t offset, int64_t count, int wide, void* __restrict__ dst) {
+    get_kernel(State s, int64_t offset, int64_t done, int64_t count, void* __restrict__ dst) {
   const int64_t stride = (int64_t)gridDim.x * kBlock;
-  const int64_t first = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  int64_t done = 0;
-  if (wide) {
-    for (int64_t k = first; k < count / 8; k += stride) {
-      const int64_t i = offset + 8 * k;
-      f32x4 a, b;
-      if constexpr (FIELD == OB_ADAMW_MASTER || BITS == 32) {
-        const float* src = FIELD == OB_ADAMW_MASTER ? s.master
-                                                    : (const float*)(FIELD == OB_ADAMW_M ? s.m : s.v);
-        a = load4(src + i);
-        b = load4(src + i + 4);
-      } else {
-        const u32x2 c = ld_stream((const u32x2*)((const uint8_t*)(FIELD == OB_ADAMW_M ? s.m : s.v) + i));
-        const uint32_t e = (FIELD == OB_ADAMW_M ? s.m_exp : s.v_exp)[i / kScaleElems];
-        a = FIELD == OB_ADAMW_M ? decode_m(c.x, e) : decode_v(c.x, e);
-        b = FIELD == OB_ADAMW_M ? decode_m(c.y, e) : decode_v(c.y, e);
-      }
-      if constexpr (BF16) {
-        st_stream((u32x4*)dst + k, u32x4{pack_bf16(a.x, a.y), pack_bf16(a.z, a.w),
-                                         pack_bf16(b.x, b.y), pack_bf16(b.z, b.w)});
-      } else {
-        st_stream((f32x4*)dst + 2 * k, a);
-        st_stream((f32x4*)dst + 2 * k + 1, b);
-      }
-    }
-    done = count / 8 * 8;
-  }
-  for (int64_t k = done + first; k < count; k += stride) {
+  for (int64_t k = done + (int64_t)blockIdx.x * kBlock + threadIdx.x; k < count; k += stride) {
     const float v = state_value<BITS, FIELD>(s, offset + k);
     if constexpr (BF16)
       ((uint16_t*)dst)[k] = (uint16_t)pack_bf16(v, 0.0f);
@@ -727,11 +813,54 @@ __global__ void __launch_bounds__(kBlock)
   }
 }
 
+// Whole blocks of 8192 elements from a multiple of 8 into a 16-byte aligned
+// dst, eight a thread and round, all of a thread's loads ahead of its stores.
+constexpr int kGetRounds = 4;
+constexpr int kGetElems = 8 * kBlock * kGetRounds;
+constexpr int64_t kGetBlocks = int64_t(1) << 22;  // of one launch, far below the grid's limit
+
+template <int BITS, int FIELD, bool BF16>
+__global__ void __launch_bounds__(kBlock)
+    get_blocks_kernel(State s, int64_t offset, void* __restrict__ dst) {
+  const int64_t first = (int64_t)blockIdx.x * (kGetElems / 8) + threadIdx.x;
+  constexpr bool kF32 = FIELD == OB_ADAMW_MASTER || BITS == 32;
+  const void* src = FIELD == OB_ADAMW_MASTER ? s.master : (FIELD == OB_ADAMW_M ? s.m : s.v);
+  f32x4 a[kGetRounds], b[kGetRounds];
+  u32x2 c[kGetRounds];
+  uint32_t e[kGetRounds];
+#pragma unroll
+  for (int r = 0; r < kGetRounds; ++r) {
+    const int64_t i = offset + 8 * (first + r * kBlock);
+    if constexpr (kF32) {
+      a[r] = load4((const float*)src + i);
+      b[r] = load4((const float*)src + i + 4);
+    } else {
+      c[r] = ld_stream((const u32x2*)((const uint8_t*)src + i));
+      e[r] = (FIELD == OB_ADAMW_M ? s.m_exp : s.v_exp)[i / kScaleElems];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kGetRounds; ++r) {
+    const int64_t k = first + r * kBlock;
+    if constexpr (!kF32) {
+      a[r] = FIELD == OB_ADAMW_M ? decode_m(c[r].x, e[r]) : decode_v(c[r].x, e[r]);
+      b[r] = FIELD == OB_ADAMW_M ? decode_m(c[r].y, e[r]) : decode_v(c[r].y, e[r]);
+    }
+    if constexpr (BF16) {
+      st_stream((u32x4*)dst + k, u32x4{pack_bf16(a[r].x, a[r].y), pack_bf16(a[r].z, a[r].w),
+                                       pack_bf16(b[r].x, b[r].y), pack_bf16(b[r].z, b[r].w)});
+    } else {
+      st_stream((f32x4*)dst + 2 * k, a[r]);
+      st_stream((f32x4*)dst + 2 * k + 1, b[r]);
+    }
+  }
+}
+
 // Whole groups of 256, one per wave and round, from fp32.
 template <int FIELD>
 __global__ void __launch_bounds__(kBlock)
     set_codes_kernel(State s, int64_t group0, int64_t groups, const float* __restrict__ src) {
-  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wave = wave_in_block();
   const int lane = threadIdx.x & 63;
   for (int64_t i = (int64_t)blockIdx.x * (kBlock / 64) + wave; i < groups;
        i += (int64_t)gridDim.x * (kBlock / 64)) {
@@ -765,61 +894,81 @@ int grid_for(int64_t threads) {
   return (int)(blocks < 1 ? 1 : (blocks > 8192 ? 8192 : blocks));
 }
 
-template <typename PT, typename GT, int BITS>
-hipError_t step_of(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
+// fn(types and kinds of the plan's step as compile-time values).
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
+struct Kind {
+  static void step(const StepPtrs& ptrs, const State& s, uint32_t t0, int64_t c0, int64_t n,
                    hipStream_t stream) {
-  if constexpr (sizeof(PT) == 2) {
-    if (s.has_master)
-      step_kernel<PT, GT, BITS, true, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
-    else if (s.stochastic)
-      step_kernel<PT, GT, BITS, false, true><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
-    else
-      step_kernel<PT, GT, BITS, false, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
-  } else {
-    step_kernel<PT, GT, BITS, false, false><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+    step_kernel<PT, GT, BITS, MASTER, SR><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
   }
+  static void small(const SmallStep& k, int64_t n, hipStream_t stream) {
+    small_step_kernel<PT, GT, BITS, MASTER, SR><<<(unsigned)n, kBlock, 0, stream>>>(k);
+  }
+};
+template <typename PT, typename GT, int BITS, typename F>
+void with_rounding(const State& s, F fn) {
+  if constexpr (sizeof(PT) == 2) {
+    if (s.has_master) return fn(Kind<PT, GT, BITS, true, false>());
+    if (s.stochastic) return fn(Kind<PT, GT, BITS, false, true>());
+  }
+  fn(Kind<PT, GT, BITS, false, false>());
+}
+template <int BITS, typename F>
+void with_types(const State& s, F fn) {
+  if (s.param_bf16)
+    s.grad_bf16 ? with_rounding<bf16, bf16, BITS>(s, fn) : with_rounding<bf16, float, BITS>(s, fn);
+  else
+    s.grad_bf16 ? with_rounding<float, bf16, BITS>(s, fn)
+                : with_rounding<float, float, BITS>(s, fn);
+}
+template <typename F>
+hipError_t with_kind(const State& s, F fn) {
+  s.state_bits == 32 ? with_types<32>(s, fn) : with_types<8>(s, fn);
   return hipGetLastError();
 }
 
+template <int BITS, int FIELD, bool BF16>
+hipError_t get_as(const State& s, int64_t offset, int64_t count, void* dst, hipStream_t stream) {
+  int64_t done = 0;
+  if (offset % 8 == 0 && (uintptr_t)dst % 16 == 0) {
+    const int64_t blocks = count / kGetElems;
+    for (int64_t at = 0; at < blocks; at += kGetBlocks) {
+      const int64_t n = blocks - at < kGetBlocks ? blocks - at : kGetBlocks;
+      get_blocks_kernel<BITS, FIELD, BF16><<<(unsigned)n, kBlock, 0, stream>>>(
+          s, offset + at * kGetElems, (char*)dst + at * kGetElems * (BF16 ? 2 : 4));
+    }
+    done = blocks * kGetElems;
+  }
+  if (done < count)
+    get_kernel<BITS, FIELD, BF16><<<grid_for(count - done), kBlock, 0, stream>>>(s, offset, done,
+                                                                              count, dst);
+  return hipGetLastError();
+}
 template <int BITS, int FIELD>
 hipError_t get_of(const State& s, int64_t offset, int64_t count, bool bf16_out, void* dst,
                   hipStream_t stream) {
-  const int wide = offset % 8 == 0 && (uintptr_t)dst % 16 == 0;
-  const int grid = grid_for(wide ? count / 8 + 8 : count);
-  if (bf16_out)
-    get_kernel<BITS, FIELD, true><<<grid, kBlock, 0, stream>>>(s, offset, count, wide, dst);
-  else
-    get_kernel<BITS, FIELD, false><<<grid, kBlock, 0, stream>>>(s, offset, count, wide, dst);
-  return hipGetLastError();
+  return bf16_out ? get_as<BITS, FIELD, true>(s, offset, count, dst, stream)
+                  : get_as<BITS, FIELD, false>(s, offset, count, dst, stream);
 }
 
 }  // namespace
 
 hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        hipStream_t stream) {
-  if (s.state_bits == 32) {
-    if (s.param_bf16)
-      return s.grad_bf16 ? step_of<bf16, bf16, 32>(s, ptrs, t0, c0, n, stream)
-                         : step_of<bf16, float, 32>(s, ptrs, t0, c0, n, stream);
-    return s.grad_bf16 ? step_of<float, bf16, 32>(s, ptrs, t0, c0, n, stream)
-                       : step_of<float, float, 32>(s, ptrs, t0, c0, n, stream);
-  }
-  if (s.param_bf16)
-    return s.grad_bf16 ? step_of<bf16, bf16, 8>(s, ptrs, t0, c0, n, stream)
-                       : step_of<bf16, float, 8>(s, ptrs, t0, c0, n, stream);
-  return s.grad_bf16 ? step_of<float, bf16, 8>(s, ptrs, t0, c0, n, stream)
-                     : step_of<float, float, 8>(s, ptrs, t0, c0, n, stream);
+  return with_kind(s, [&](auto kind) { kind.step(ptrs, s, t0, c0, n, stream); });
+}
+
+hipError_t launch_small(const SmallStep& k, int64_t n, hipStream_t stream) {
+  return with_kind(k.s, [&](auto kind) { kind.small(k, n, stream); });
 }
 
 hipError_t launch_norm(const State& s, const NormPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        int64_t at, bool keep, hipStream_t stream) {
   const unsigned grid = (unsigned)norm_partials(n);
-  const int64_t kept = keep ? kKeptBytes / (kChunkElems * (s.grad_bf16 ? 2 : 4)) : 0;
-  if (s.grad_bf16)
-    norm_kernel<bf16><<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, kept, s.partials + at);
-  else
-    norm_kernel<float><<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, kept,
-                                                    s.partials + at);
+  const int64_t kept = kKeptBytes / (kChunkElems * (s.grad_bf16 ? 2 : 4));
+  const auto kernel = s.grad_bf16 ? (keep ? norm_kernel<bf16, true> : norm_kernel<bf16, false>)
+                                  : (keep ? norm_kernel<float, true> : norm_kernel<float, false>);
+  kernel<<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, kept, s.partials + at);
   return hipGetLastError();
 }
 

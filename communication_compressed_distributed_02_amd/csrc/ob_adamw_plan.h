@@ -25,6 +25,9 @@ constexpr int kMaxGroups = OB_ADAMW_MAX_GROUPS;
 constexpr int kPtrsPerStep = 240;
 constexpr int kPtrsPerNorm = 480;
 constexpr int kNormBlocks = 2048;   // partial sums of one launch of the norm, at most
+// A step of at most so many chunks (262144 elements) is one launch, its chunks
+// and pointers among the arguments.
+constexpr int kSmallChunks = 64;
 constexpr int32_t kMaxTensors = 1 << 20;
 constexpr int64_t kMaxLength = int64_t(1) << 40;  // of a state array; no size below can overflow
 constexpr int kNumGuards = 8;
@@ -140,6 +143,7 @@ struct Plan {
   int64_t n_partials = 0;
   std::vector<int64_t> numel;
   std::vector<Span> step_spans, norm_spans;
+  std::vector<ChunkRec> small;  // the chunks, where they are few enough
   // the pointers that passed the checks last, and room for the check
   std::vector<const void*> seen_p, seen_g;
   std::vector<Range> ranges;
@@ -167,6 +171,7 @@ struct Plan {
       }
       row += rows_of(numel[i]);
     }
+    if (recs->size() <= kSmallChunks) small = *recs;
     list_spans(kPtrsPerStep, &step_spans);
     list_spans(kPtrsPerNorm, &norm_spans);
     for (const Span& s : norm_spans) n_partials += norm_partials(s.chunks);
