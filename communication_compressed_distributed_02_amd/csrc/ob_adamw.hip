@@ -281,6 +281,11 @@ ob_status ob_adamw_grad_norm(ob_adamw_t h, const void* const* grads, float grad_
     return OB_ERR_ARG;
   st = h->plan.check_grads(grads);
   if (st != OB_OK) return st;
+  if (h->plan.small) {
+    aw::SmallNorm k{h->st.recs, h->st.control, h->st.partials, sumsq, norm, grad_scale, {}};
+    for (int32_t i = 0; i < h->plan.cfg.n_tensors; ++i) k.g[i] = grads[i];
+    return fail(h, aw::launch_small_norm(k, h->st.grad_bf16, h->plan.chunks, h->stream));
+  }
   hipError_t e = norm_pass(h, grads, false);
   if (e == hipSuccess)
     e = aw::launch_norm_finish(h->st, h->plan.n_partials, grad_scale, sumsq, norm, h->stream);
@@ -315,17 +320,15 @@ ob_status ob_adamw_step(ob_adamw_t h, const void* const* params, const void* con
     c.partials = h->st.partials;
     c.n_partials = h->plan.n_partials;
   }
-  const std::vector<aw::ChunkRec>& few = h->plan.small;
-  if (e == hipSuccess && !few.empty()) {
+  if (e == hipSuccess && h->plan.small) {
     aw::SmallStep k;
     k.s = h->st;
     k.a = c;
-    for (size_t i = 0; i < few.size(); ++i) {
-      const aw::ChunkRec& r = few[i];
-      k.rec[i] = {grads[r.tensor], const_cast<void*>(params[r.tensor]), r.row, r.state_row,
-                  r.count, r.group};
+    for (int32_t i = 0; i < h->plan.cfg.n_tensors; ++i) {
+      k.g[i] = grads[i];
+      k.p[i] = const_cast<void*>(params[i]);
     }
-    return fail(h, aw::launch_small(k, (int64_t)few.size(), h->stream));
+    return fail(h, aw::launch_small(k, h->plan.chunks, h->stream));
   }
   if (e == hipSuccess) e = aw::launch_control(h->st, c, h->stream);
   for (size_t i = 0; i < h->plan.step_spans.size() && e == hipSuccess; ++i) {

@@ -27,7 +27,8 @@ struct Control {
   double p1, p2;             // b1^steps, b2^steps
   float gscale, rbc2;
   uint32_t skip, k0, k1;
-  uint32_t ticket;           // waves of a small step that have read the above
+  uint32_t root;             // tickets of small launches: leaves that are done
+  uint32_t leaf[kLeaves][16];  // and tickets taken, each counter in a line of its own
   float decay[kMaxGroups], rate[kMaxGroups];
 };
 
@@ -56,23 +57,29 @@ struct State {
   int32_t param_bf16, grad_bf16, state_bits, has_master, stochastic;
 };
 
-// A small step's work, in the arguments of its one launch: each chunk with
-// its own pointers.
-struct SmallRec {
-  const void* g;
-  void* p;
-  uint32_t row, state_row;
-  uint16_t count, group;
-};
+// The launches over few chunks.
 struct SmallStep {
   State s;
   ControlArgs a;
-  SmallRec rec[kSmallChunks];
+  const void* g[kSmallTensors];
+  void* p[kSmallTensors];
 };
-static_assert(sizeof(SmallStep) <= 4096, "kernel arguments");
+struct SmallNorm {
+  const ChunkRec* recs;
+  Control* control;
+  double* partials;
+  double* sumsq;
+  float* norm;
+  float grad_scale;
+  const void* g[kSmallTensors];
+};
+static_assert(sizeof(SmallStep) <= 4096 && sizeof(StepPtrs) + sizeof(State) + 16 <= 4096,
+              "kernel arguments");
 
 // A step of n <= kSmallChunks chunks: control and update in one launch.
-hipError_t launch_small(const SmallStep& p, int64_t n, hipStream_t stream);
+hipError_t launch_small(const SmallStep& k, int64_t n, hipStream_t stream);
+// S and the norm of n <= kSmallChunks chunks in one launch.
+hipError_t launch_small_norm(const SmallNorm& k, bool grad_bf16, int64_t n, hipStream_t stream);
 // Chunks [c0, c0 + n) of tensors t0, t0 + 1, ... whose pointers `ptrs` holds.
 hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        hipStream_t stream);

@@ -546,9 +546,37 @@ __global__ void __launch_bounds__(kBlock)
 __device__ __forceinline__ double block_sum(double acc, double* red) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) acc = acc + __shfl_xor(acc, o, 64);
+  __syncthreads();  // red may still be read from the call before
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
   __syncthreads();
   return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__device__ __forceinline__ double add_squares(double acc, const f32x4 (&v)[kGroups]) {
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const double d = (double)v[u][k];  // the square is exact in fp64
+      acc = __builtin_fma(d, d, acc);
+    }
+  }
+  return acc;
+}
+
+// Sum of this lane's squares of a row, `left` of whose elements there are.
+template <typename GT>
+__device__ __forceinline__ double row_sum(const GT* p, int left, int at) {
+  f32x4 v[kGroups];
+  if (left >= kRowElems) {
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) v[u] = load4(p + u * kScaleElems);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) v[u] = load_some(p + u * kScaleElems,
+                                                       left - u * kScaleElems - at);
+  }
+  return add_squares(0.0, v);
 }
 
 // In front of a step (kept > 0) a span's chunks go from the last to the first,
@@ -593,14 +621,7 @@ __global__ void __launch_bounds__(kBlock)
       rec = recs[chunk(i)];
       g = (const GT*)ptrs.g[rec.tensor - t0];
     }
-#pragma unroll
-    for (int u = 0; u < kGroups; ++u) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const double d = (double)v[u][k];  // the square is exact in fp64
-        acc = __builtin_fma(d, d, acc);
-      }
-    }
+    acc = add_squares(acc, v);
   }
   acc = block_sum(acc, red);
   if (threadIdx.x == 0) partials[blockIdx.x] = acc;
@@ -696,7 +717,26 @@ __global__ void __launch_bounds__(kBlock) control_kernel(Control* c, ControlArgs
   c->p2 = d.p2;
 }
 
-// ------------------------------------------------------------ small steps --
+// ---------------------------------------------------------- small launches --
+// True for the last of `all` callers: each adds `one` (1) once, in one counter
+// where they are few, else over kLeaves of them whose last callers meet at a
+// root (a counter takes an atomic every 12 ns).  The counters are left at 0.
+// `id` numbers the callers from 0.
+template <int ORDER>
+__device__ __forceinline__ bool last_ticket(Control* c, uint32_t id, uint32_t all, uint32_t one) {
+  const uint32_t leaves = all > 64 ? kLeaves : 1;
+  const uint32_t leaf = id % leaves;
+  const uint32_t n = __hip_atomic_fetch_add(&c->leaf[leaf][0], one, ORDER,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+  if (n != (all + leaves - 1 - leaf) / leaves - 1) return false;
+  c->leaf[leaf][0] = 0;
+  if (leaves == 1) return true;
+  if (__hip_atomic_fetch_add(&c->root, 1u, ORDER, __HIP_MEMORY_SCOPE_AGENT) != leaves - 1)
+    return false;
+  c->root = 0;
+  return true;
+}
+
 // Control and update in one launch, for the latency of steps over few
 // elements.  Every wave derives the scalars for itself from the counts before
 // the step while its row is being loaded, and takes a ticket once it has
@@ -709,7 +749,9 @@ __device__ __forceinline__ T ld_shared_state(const T* p) {
 
 template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
 __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
-  const SmallRec rec = k.rec[blockIdx.x];
+  const ChunkRec rec = k.s.recs[blockIdx.x];
+  const GT* g = (const GT*)k.g[rec.tensor];
+  PT* p = (PT*)k.p[rec.tensor];
   const ControlArgs& a = k.a;
   Control* ctl = k.s.control;
   const int lane = threadIdx.x & 63;
@@ -719,7 +761,7 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
   const double p1 = ld_shared_state(&ctl->p1), p2 = ld_shared_state(&ctl->p2);
   double part = 0.0;
   if (a.partials != nullptr) {
-    if (lane < (int)a.n_partials) part = a.partials[lane];
+    for (int i = lane; i < (int)a.n_partials; i += 64) part = part + a.partials[i];
   } else if (a.sumsq != nullptr && lane == 0) {
     part = *a.sumsq;
   }
@@ -736,12 +778,10 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
     c.skip = d.skip;
     if (lane == 0) {
       // What is added depends on the loaded counts, so the ticket is taken
-      // after they have arrived; steps is never negative.
+      // after they have arrived; none of them is ever negative.
       const uint32_t one = steps >= 0 && p1 >= 0.0 && p2 >= 0.0 ? 1u : 2u;
-      const uint32_t n = __hip_atomic_fetch_add(&ctl->ticket, one, __ATOMIC_RELAXED,
-                                                __HIP_MEMORY_SCOPE_AGENT);
-      if (n == gridDim.x * (kBlock / 64) - 1) {
-        ctl->ticket = 0;
+      if (last_ticket<__ATOMIC_RELAXED>(ctl, blockIdx.x * (kBlock / 64) + wave,
+                                        gridDim.x * (kBlock / 64), one)) {
         if (a.norm != nullptr) *a.norm = (float)d.norm;
         if (d.skip) {
           ctl->skipped += 1;
@@ -754,12 +794,36 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
     }
     return c;
   };
-  if (rec.g == nullptr || left <= 0) {
+  if (g == nullptr || left <= 0) {
     scalars();
     return;
   }
-  step_wave<PT, GT, BITS, MASTER, SR>((const GT*)rec.g, (PT*)rec.p, k.s, rec.row, rec.state_row,
-                                      wave, left, scalars);
+  step_wave<PT, GT, BITS, MASTER, SR>(g, p, k.s, rec.row, rec.state_row, wave, left, scalars);
+}
+
+// A chunk a block; the block with the last ticket, which each takes behind
+// its partial sum, folds the sums.
+template <typename GT>
+__global__ void __launch_bounds__(kBlock) small_norm_kernel(SmallNorm k) {
+  __shared__ double red[kBlock / 64];
+  __shared__ bool last;
+  const ChunkRec rec = k.recs[blockIdx.x];
+  const GT* g = (const GT*)k.g[rec.tensor];
+  const int wave = wave_in_block();
+  const int at = (threadIdx.x & 63) * 4;
+  const int left = g == nullptr ? 0 : (int)rec.count - wave * kRowElems;
+  const double acc = block_sum(row_sum(g + ((int64_t)rec.row + wave) * kRowElems + at, left, at),
+                               red);
+  if (threadIdx.x == 0) {
+    k.partials[blockIdx.x] = acc;
+    last = last_ticket<__ATOMIC_ACQ_REL>(k.control, blockIdx.x, gridDim.x, 1u);
+  }
+  __syncthreads();
+  if (!last) return;
+  const double total = fold_partials(k.partials, gridDim.x, red);
+  if (threadIdx.x != 0) return;
+  if (k.sumsq != nullptr) *k.sumsq = total;
+  if (k.norm != nullptr) *k.norm = (float)(sqrt(total) * (double)k.grad_scale);
 }
 
 __global__ void set_steps_kernel(Control* c, int64_t steps, double p1, double p2) {
@@ -980,6 +1044,14 @@ hipError_t launch_control(const State& s, const ControlArgs& a, hipStream_t stre
 hipError_t launch_norm_finish(const State& s, int64_t n_partials, float grad_scale, double* sumsq,
                               float* norm, hipStream_t stream) {
   norm_finish_kernel<<<1, kBlock, 0, stream>>>(s.partials, n_partials, grad_scale, sumsq, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_small_norm(const SmallNorm& k, bool grad_bf16, int64_t n, hipStream_t stream) {
+  if (grad_bf16)
+    small_norm_kernel<bf16><<<(unsigned)n, kBlock, 0, stream>>>(k);
+  else
+    small_norm_kernel<float><<<(unsigned)n, kBlock, 0, stream>>>(k);
   return hipGetLastError();
 }
 
