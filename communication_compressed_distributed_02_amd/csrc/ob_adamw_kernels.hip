@@ -250,33 +250,17 @@ __device__ __forceinline__ void clear_behind(int n, f32x4& m, f32x4& v, f32x4& x
     if (k >= n) m[k] = v[k] = x[k] = 0.0f;
 }
 
-// The same in fewer instructions, for 2^-30 <= eps, v < 2^100 and |m| < 2^90:
-// a square root and a quotient by Newton steps from v_rsq_f32 and v_rcp_f32
-// without the scaling for ranges that cannot occur.  Both round correctly
-// where v is 0 or at least 2^-96 and |m| at least 2^-100; below, an ulp of
-// sqrt(v) is far below eps's, and an ulp of the quotient far below x's.  The
-// 8-bit step is bound by the ALU with the general forms: with these, and
-// without the exceptions in decoding and encoding, 1.56B bfloat16 parameters
-// take 2.65 ms (5.9 TB/s) against 3.10 ms.
-__device__ __forceinline__ float root(float v) {
-  v = fmaxf(v, 0x1p-126f);  // 0: 2^-63 is below half an ulp of eps even times rbc2
-  const float r = __builtin_amdgcn_rsqf(v);
-  float s = v * r, h = 0.5f * r;
-  const float e = __builtin_fmaf(-h, s, 0.5f);
-  h = __builtin_fmaf(h, e, h);
-  s = __builtin_fmaf(s, e, s);
-  return __builtin_fmaf(__builtin_fmaf(-s, s, v), h, s);
-}
-__device__ __forceinline__ float quotient(float m, float den) {
-  float r = __builtin_amdgcn_rcpf(den);
-  r = __builtin_fmaf(__builtin_fmaf(-den, r, 1.0f), r, r);
-  float q = m * r;
-  q = __builtin_fmaf(__builtin_fmaf(-den, q, m), r, q);
-  return __builtin_fmaf(__builtin_fmaf(-den, q, m), r, q);
-}
+// The same beside 8-bit moments, whose own steps are 2^-4 of them, for 2^-30
+// <= eps, v < 2^100 and |m| < 2^90: v_sqrt_f32 and v_rcp_f32 as they are (an
+// ulp each, so m/den is within 7 roundings; below 2^-126 v counts as 0, which
+// eps hides), without the scaling and the Newton steps of the general forms.
+// The step is bound by the ALU otherwise: 1.56B bfloat16 parameters take
+// 3.10 ms in the general form, 2.65 with correctly rounded results but no
+// scaling, and 2.49 (6.3 TB/s) as here.
 __device__ __forceinline__ float updated_plain(float x, float m, float v, float decay, float rate,
                                                float rbc2, float eps) {
-  return (x * decay) - (rate * quotient(m, (root(v) * rbc2) + eps));
+  const float den = (__builtin_amdgcn_sqrtf(v) * rbc2) + eps;
+  return (x * decay) - (rate * (m * __builtin_amdgcn_rcpf(den)));
 }
 
 // Four elements as they were loaded: bfloat16 stays packed until it is used.
@@ -627,10 +611,18 @@ __global__ void __launch_bounds__(kBlock)
   if (threadIdx.x == 0) partials[blockIdx.x] = acc;
 }
 
-// Sum of n partials by one block, in an order fixed by n.
+// Sum of n partials by one block, in an order fixed by n.  Eight loads are
+// under way at a time: with one, 2048 partials took 5 us, a tenth of a clipped
+// step over 13M parameters.
 __device__ __forceinline__ double fold_partials(const double* partials, int64_t n, double* red) {
   double acc = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kBlock) acc = acc + partials[i];
+  for (int64_t i = threadIdx.x; i < n; i += 8 * kBlock) {
+    double p[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = i + k * kBlock < n ? partials[i + k * kBlock] : 0.0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc = acc + p[k];
+  }
   return block_sum(acc, red);
 }
 

@@ -38,6 +38,10 @@
  *    (m: 0x7f or 0xff, v: 255) and leaves its block's exponents alone.
  *    Rounding v to nearest would freeze it: a step moves v by about 1 - b2 of
  *    itself, the codes are 6 to 12 % apart.
+ *    Beside 8-bit states the square root and the quotient are formed from
+ *    one-ulp approximations (for 2^-30 <= eps), so that m / (...) is within
+ *    7 * 2^-24 of its exact value, relatively; everything else rounds as
+ *    stated.
  *  - random bits: 32-bit words hashed from k/4 (k = the element's index in
  *    the state), the seed and the step count; elements 4i .. 4i+3 take the
  *    low and the high half of word 0, then of word 1, for v, and of words 2

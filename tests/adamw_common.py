@@ -10,6 +10,14 @@ relative), for g' exact and first-order in u:
        so m/den carries |dm|/den + 7u|m|/den, and the rate (rounded) and the
        product 2u more: 9u |up| + rate |dm|/den
   x: decay rounded, product, difference: 3u|x| + u|up| on top
+
+Beside 8-bit states the kernels take the square root and the reciprocal from
+instructions of one ulp (2u) each.  From the same m and v, then: sqrt 2u, the
+factor u, eps's sum u, the reciprocal 2u, the product u, the rate u, against u
+for each of the five operations in the form below: 8u + 5u of the update, and
+the final difference rounds u|x| on either side, so 2u|x| + 13u|up|; 14u covers
+the higher orders.  The rounding to bfloat16 is monotone, so a parameter lies
+between the roundings of the two ends.
 """
 import math
 
@@ -185,9 +193,33 @@ class Reference:
         self.master = [p.copy() for p in self.x] if master else None
         z = [np.zeros(p.size, F) for p in self.x]
         self.m, self.v = z, [a.copy() for a in z]
+        # what the last step rounded to the parameter, and how far it moved it
+        self.exact, self.up = [None] * len(params), [None] * len(params)
         if bits == 8:
             self.m = [encode_m(a) for a in z]
             self.v = [encode_v(a, 0) for a in z]
+
+    def bounds(self, i):
+        """The least and the greatest value that tensor i may have."""
+        if self.bits == 32 or self.up[i] is None:
+            x = self.x[i] if self.master is None else self.master[i]
+            return x, x
+        with np.errstate(all="ignore"):
+            x = self.exact[i].astype(np.float64)
+            d = U * (2 * np.abs(x) + 14 * np.abs(self.up[i].astype(np.float64)))
+            ends = []
+            for side in (-1, 1):
+                y = np.nextafter((x + side * d).astype(F), F(side * np.inf))  # outwards
+                y = np.where(np.isfinite(x), y, self.exact[i])
+                ends.append(y if self.master is not None else self.rounded(i, y))
+        return ends
+
+    def rounded(self, i, x):
+        if self.param == "f32":
+            return x
+        if self.stochastic:
+            return bf16_stochastic(x, random16(self.offsets[i], x.size, self.seed, self.t, 2))
+        return bf16_nearest(x)
 
     def norm(self, grads, scale=1.0):
         s = sum(float(np.dot(g.astype(np.float64), g.astype(np.float64))) for g in grads
@@ -216,14 +248,11 @@ class Reference:
                 r = random16(off, x.size, self.seed, self.t, 0)
                 m, v = encode_m(m), encode_v(v, r * 16 + 8)
             self.m[i], self.v[i] = m, v
+            with np.errstate(all="ignore"):
+                self.exact[i], self.up[i] = x, x - old * (F(1) - F(float(F(a)) * float(F(b))))
             if self.master is not None:
                 self.master[i] = x
-            if self.param == "f32":
-                self.x[i] = x
-            elif self.stochastic:
-                self.x[i] = bf16_stochastic(x, random16(off, x.size, self.seed, self.t, 2))
-            else:
-                self.x[i] = bf16_nearest(x)
+            self.x[i] = self.rounded(i, x)
 
 
 def same(a, b):
