@@ -21,8 +21,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
 
 
 PROBE_LIB = os.path.join(PKG, "libob_probe.so")
-PROBE_SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
-                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
+PROBE_SOURCES = [os.path.join(CSRC, "ob_probe.hip")]
 
 
 def build(extra_flags=(), out=LIB):
@@ -42,8 +41,7 @@ def build_probe(out=PROBE_LIB):
 
 
 MATHCHECK_LIB = os.path.join(PKG, "libob_mathcheck.so")
-MATHCHECK_SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
-                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
+MATHCHECK_SOURCES = [os.path.join(CSRC, "ob_mathcheck.hip")]
 
 
 def build_mathcheck(out=MATHCHECK_LIB):
