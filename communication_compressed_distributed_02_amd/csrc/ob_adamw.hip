@@ -420,6 +420,12 @@ ob_status ob_adamw_check_guards(ob_adamw_t h, int32_t* first_bad) {
   return OB_OK;
 }
 
+ob_status ob_adamw_set_stream(ob_adamw_t h, void* stream) {
+  if (h == nullptr) return OB_ERR_ARG;
+  h->stream = (hipStream_t)stream;
+  return OB_OK;
+}
+
 ob_status ob_adamw_destroy(ob_adamw_t h) {
   if (h == nullptr) return OB_ERR_ARG;
   delete h;

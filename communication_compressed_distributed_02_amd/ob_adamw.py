@@ -19,7 +19,7 @@ OB_ADAMW_MAX_GROUPS = 32
 EXPORTED = ("ob_adamw_layout", "ob_adamw_init", "ob_adamw_attach", "ob_adamw_grad_norm",
             "ob_adamw_step", "ob_adamw_get_state", "ob_adamw_set_state", "ob_adamw_state",
             "ob_adamw_set_steps", "ob_adamw_get_steps", "ob_adamw_check_guards",
-            "ob_adamw_destroy")
+            "ob_adamw_set_stream", "ob_adamw_destroy")
 
 FIELDS = {"m": OB_ADAMW_M, "v": OB_ADAMW_V, "master": OB_ADAMW_MASTER, "m_exp": OB_ADAMW_M_EXP,
           "v_exp": OB_ADAMW_V_EXP}
@@ -63,6 +63,7 @@ def _declare(L):
         "ob_adamw_set_steps": [P, I64],
         "ob_adamw_get_steps": [P, i64s, i64s],
         "ob_adamw_check_guards": [P, i32s],
+        "ob_adamw_set_stream": [P, P],
         "ob_adamw_destroy": [P],
     }
     for name, args in sig.items():
@@ -154,6 +155,10 @@ def ob_adamw_check_guards(h):
     return bad.value
 
 
+def ob_adamw_set_stream(h, stream_ptr):
+    _check(_lib.ob_adamw_set_stream(h, stream_ptr), "ob_adamw_set_stream")
+
+
 def ob_adamw_destroy(h):
     _check(_lib.ob_adamw_destroy(h), "ob_adamw_destroy")
 
@@ -210,12 +215,22 @@ class _Plan(OnStream):
 
     def _call(self, tensors, fn, *args):
         """fn(*args) with this plan's device current, ordered with the
-        caller's stream."""
+        caller's stream.  On a stream under capture the call is recorded there
+        (the plan's own stream may be the default one, which cannot take part
+        in a capture)."""
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                self._ordered(tensors, fn, *args)
-        elif _current_stream(self.device.index) == self._stream_ptr:
+                self._call(tensors, fn, *args)
+            return
+        current = _current_stream(self.device.index)
+        if current == self._stream_ptr:
             fn(*args)
+        elif torch.cuda.is_current_stream_capturing():
+            ob_adamw_set_stream(self.h, current)
+            try:
+                fn(*args)
+            finally:
+                ob_adamw_set_stream(self.h, self._stream_ptr)
         else:
             self._ordered(tensors, fn, *args)
 

@@ -1,4 +1,10 @@
-"""1-bit Adam over a list of ragged parameter tensors, n simulated workers.
+"""torch.optim front ends of the library's optimizers.
+
+OneBitAdamOptimizer: 1-bit Adam over a list of ragged parameter tensors, n
+simulated workers (below).  AdamWOptimizer: AdamW over parameters where they
+lie, with states in 32 bits or in 8 (its own docstring).
+
+1-bit Adam over a list of ragged parameter tensors, n simulated workers.
 
 The parameters are moved once into the library's flat fp32 parameter buffer
 and rebound as views of it, and every worker gets one flat gradient buffer
@@ -22,6 +28,7 @@ state (workspace bytes and step counters), so a run resumes bit-identically.
 import torch
 
 from . import ob_adam as ob
+from . import ob_adamw as oa
 
 
 def flat_layout(numels, n_workers):
@@ -139,3 +146,98 @@ class OneBitAdamOptimizer(torch.optim.Optimizer):
         self._bind_params()
         self.t = state["t"]
         g["lr"] = state["lr"]
+
+
+class AdamWOptimizer(torch.optim.Optimizer):
+    """AdamW over parameters that stay where they are: contiguous float32 or
+    bfloat16 tensors of one type on one GPU, their .grad of `grad_dtype`
+    (default the same type).
+
+    Groups may differ in lr and weight_decay, which are read from param_groups
+    at every step, so torch's LR schedulers drive it; betas and eps are common.
+    state_bits, master, stochastic and seed as for ob_adamw.AdamW.  max_norm: clip
+    by the global gradient norm (0: no clipping), without a host wait; the last
+    norm is in `norm` on the device.  skip_nonfinite: a step whose gradients are
+    not all finite changes nothing.  A parameter without a gradient is left as it
+    is.  state_dict() / load_state_dict() carry the library's whole state."""
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
+                 state_bits=32, master=False, stochastic=False, grad_dtype=None, max_norm=0.0,
+                 skip_nonfinite=False, seed=0, stream=None):
+        self._core = None
+        super().__init__(params, dict(lr=lr, weight_decay=weight_decay))
+        self.params = [p for g in self.param_groups for p in g["params"]]
+        groups = [i for i, g in enumerate(self.param_groups) for _ in g["params"]]
+        self.max_norm, self.skip_nonfinite, self.norm = max_norm, skip_nonfinite, None
+        self._make = lambda checkpoint=None: oa.AdamW(
+            [p.detach() for p in self.params], groups, len(self.param_groups), grad_dtype,
+            state_bits, master, stochastic, betas, eps, seed, stream=stream,
+            checkpoint=checkpoint)
+        self._core = self._make()
+
+    @property
+    def core(self):
+        """The ob_adamw.AdamW behind it."""
+        return self._core
+
+    def add_param_group(self, param_group):
+        if self._core is not None:
+            raise ValueError("the parameters are fixed when the optimizer is made")
+        for k in param_group:
+            if k not in ("params", "lr", "weight_decay"):
+                raise ValueError("a group has its own lr and weight_decay only, not " + k)
+        super().add_param_group(param_group)
+
+    def grads(self):
+        """The parameters' gradients as the library takes them."""
+        out = []
+        for p in self.params:
+            g = p.grad
+            if g is not None:
+                if g.is_sparse:
+                    raise ValueError("sparse gradients are not supported")
+                g = g.detach().contiguous()
+            out.append(g)
+        return out
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=1.0, lr=None, sumsq=None):
+        """One step.  grad_scale: multiplies the gradients (1 / loss scale, 1 /
+        accumulated passes).  lr: one rate per group in place of the groups' own, for
+        a captured step a float32 device tensor.  sumsq: the squared norm to clip
+        and skip by (a sum over ranks) as a float64 device scalar."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        if lr is None:
+            lr = [float(g["lr"]) for g in self.param_groups]
+        grads = self.grads()
+        # the parameters as they lie now
+        batch = self._core.bind(grads, [p.detach() for p in self.params])
+        self.norm = self._core.step(batch, lr, [g["weight_decay"] for g in self.param_groups],
+                                    self.max_norm, grad_scale, self.skip_nonfinite, sumsq)
+        torch.autograd.graph.increment_version(
+            [p for p, g in zip(self.params, grads) if g is not None])
+        return loss
+
+    @property
+    def steps(self):
+        """(steps taken, steps skipped); waits for the GPU."""
+        return self._core.steps
+
+    def state_dict(self):
+        """The library's state (workspace bytes on the CPU) and the groups' rates."""
+        return {"workspace": self._core.checkpoint("cpu"), "numels": list(self._core.numels),
+                "param_groups": [{k: v for k, v in g.items() if k != "params"}
+                                 for g in self.param_groups]}
+
+    def load_state_dict(self, state):
+        """A state_dict() of an optimizer made with the same arguments over
+        parameters of the same sizes."""
+        if (state["numels"] != list(self._core.numels)
+                or len(state["param_groups"]) != len(self.param_groups)):
+            raise ValueError("state of other parameters")
+        self._core = self._make(state["workspace"])
+        for g, saved in zip(self.param_groups, state["param_groups"]):
+            g.update(saved)

@@ -53,7 +53,8 @@
  *
  * Ownership, streams and errors as in ob_adam.h: the caller owns all device
  * memory, the library allocates none; every call is enqueued on the stream
- * given to ob_adamw_init and returns without waiting, except where stated;
+ * given to ob_adamw_init (or ob_adamw_set_stream) and returns without waiting,
+ * except where stated;
  * argument errors return before anything is enqueued and leave the state
  * untouched; a HIP error returns OB_ERR_HIP and poisons the handle.  The
  * handle's device (the one the workspace lies on) has to be the current one,
@@ -184,6 +185,10 @@ ob_status ob_adamw_get_steps(ob_adamw_t h, int64_t* steps, int64_t* skipped);
  * order: control block, chunk records, partial sums, m, v, m exponents, v
  * exponents, master copies).  Waits for the stream. */
 ob_status ob_adamw_check_guards(ob_adamw_t h, int32_t* first_bad);
+
+/* Enqueue later calls on `stream` (of the plan's device), as to record one on a
+ * stream under capture.  The caller orders them after the earlier ones. */
+ob_status ob_adamw_set_stream(ob_adamw_t h, void* stream);
 
 /* Release the handle (the caller frees the workspace afterwards). */
 ob_status ob_adamw_destroy(ob_adamw_t h);

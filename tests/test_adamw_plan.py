@@ -192,7 +192,7 @@ def test_refusals_before_any_device_call(oa):
     assert status(oa.ob_adamw_init, cfg, [100], [2], 256, need, None, None) == ARG
     assert status(oa.ob_adamw_init, cfg, [100], [-1], 256, need, None, None) == ARG
     for fn, args in ((oa.ob_adamw_get_steps, ()), (oa.ob_adamw_set_steps, (1,)),
-                     (oa.ob_adamw_check_guards, ()), (oa.ob_adamw_state, (0,)),
+                     (oa.ob_adamw_check_guards, ()), (oa.ob_adamw_set_stream, (None,)), (oa.ob_adamw_state, (0,)),
                      (oa.ob_adamw_get_state, (0, 0, 1, 0, None)),
                      (oa.ob_adamw_set_state, (0, 0, 1, None)),
                      (oa.ob_adamw_grad_norm, (None, 1.0, None, None)),
