@@ -263,10 +263,16 @@ class _Plan(OnStream):
                    sumsq.data_ptr(), norm.data_ptr())
         return norm, sumsq
 
+    def _wait(self, fn):
+        """fn(handle), a call that waits for the stream."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+        with torch.cuda.device(self.device):
+            return fn(self.h)
+
     def check_guards(self):
         """-1 if no kernel wrote past a workspace buffer (synchronizes)."""
-        with torch.cuda.device(self.device):
-            return ob_adamw_check_guards(self.h)
+        return self._wait(ob_adamw_check_guards)
 
     def close(self):
         if self.h:
@@ -352,7 +358,7 @@ class AdamW(_Plan):
                            params, self._ptrs(params, self.param_dtype, "parameters", False))
 
     def _per_group(self, values, into, what):
-        if isinstance(values, (int, float)):
+        if not hasattr(values, "__len__"):
             for i in range(self.n_groups):
                 into[i] = values
             return
@@ -451,8 +457,7 @@ class AdamW(_Plan):
     @property
     def steps(self):
         """(steps taken, steps skipped), replays among them (synchronizes)."""
-        with torch.cuda.device(self.device):
-            return ob_adamw_get_steps(self.h)
+        return self._wait(ob_adamw_get_steps)
 
     def checkpoint(self, device="cpu"):
         """A copy of the workspace bytes: the whole optimizer state."""

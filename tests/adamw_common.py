@@ -152,7 +152,7 @@ def scalars(t, lr, wd, gs=1.0):
     return F(gs), F(1.0 - lr * wd), F(lr / (1.0 - p1)), F(1.0 / math.sqrt(1.0 - p2))
 
 
-def step32(x, m, v, g, t, lr, wd, gs=1.0):
+def step32(x, m, v, g, t, lr, wd, gs=1.0, eps=EPS):
     """fp32, one rounding per operation: new x, m, v."""
     x, m, v, g = (np.asarray(a, F) for a in (x, m, v, g))
     gs, decay, rate, rbc2 = scalars(t, lr, wd, gs)
@@ -160,7 +160,7 @@ def step32(x, m, v, g, t, lr, wd, gs=1.0):
         g = g * gs
         m = (B1 * m) + (OB1 * g)
         v = (B2 * v) + (OB2 * (g * g))
-        x = (x * decay) - (rate * (m / ((np.sqrt(v) * rbc2) + EPS)))
+        x = (x * decay) - (rate * (m / ((np.sqrt(v) * rbc2) + eps)))
     return x, m, v
 
 
@@ -185,7 +185,8 @@ class Reference:
     """The fp32 form over a list of tensors, as the library's plan runs it."""
 
     def __init__(self, params, offsets, bits=32, param="f32", master=False, stochastic=False,
-                 groups=None, seed=0, steps=0):
+                 groups=None, seed=0, steps=0, eps=EPS):
+        self.eps = F(eps)
         self.x = [np.asarray(p, F).copy() for p in params]
         self.offsets, self.bits, self.param = offsets, bits, param
         self.stochastic, self.seed, self.t = stochastic, seed, steps
@@ -201,7 +202,8 @@ class Reference:
 
     def bounds(self, i):
         """The least and the greatest value that tensor i may have."""
-        if self.bits == 32 or self.up[i] is None:
+        # below 2^-30 the library keeps the correctly rounded forms
+        if self.bits == 32 or self.up[i] is None or self.eps < 2.0 ** -30:
             x = self.x[i] if self.master is None else self.master[i]
             return x, x
         with np.errstate(all="ignore"):
@@ -242,7 +244,7 @@ class Reference:
             if self.bits == 8:
                 m, v = decode_m(*m), decode_v(*v)
             old = self.master[i] if self.master is not None else self.x[i]
-            x, m, v = step32(old, m, v, g, self.t, a, b, gs)
+            x, m, v = step32(old, m, v, g, self.t, a, b, gs, self.eps)
             off = self.offsets[i]
             if self.bits == 8:
                 r = random16(off, x.size, self.seed, self.t, 0)

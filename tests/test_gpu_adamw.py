@@ -328,6 +328,73 @@ def test_first_and_extreme_hyperparameters(oa):
         assert np.all(np.abs(host(xs[0]) - x) <= tol), betas
 
 
+def test_small_eps_keeps_the_rounded_forms_beside_8_bits(oa):
+    params, grads = make_inputs([1, 2048, 4096, 5000], 19, 4)
+    xs = [dev(a) for a in params]
+    opt = oa.AdamW(xs, state_bits=8, eps=1e-12, seed=4)
+    ref = A.Reference(params, opt.offsets, 8, seed=4, eps=1e-12)
+    for t, gs in enumerate(grads):
+        opt.step([dev(a) for a in gs], np.float32(1e-2), 0.1)
+        ref.step(gs, 1e-2, 0.1)
+        assert_state(opt, ref, "step %d" % t)
+
+
+def test_plan_without_elements(oa):
+    """Only empty tensors: the step counts, the norm is 0."""
+    import torch
+    xs = [torch.zeros(0, device="cuda"), torch.zeros(0, 3, device="cuda")]
+    for bits in (32, 8):
+        opt = oa.AdamW(xs, state_bits=bits)
+        norm = opt.step([torch.zeros(0, device="cuda"), None], 1e-3, max_norm=1.0)
+        assert float(norm) == 0.0 and opt.steps == (1, 0) and opt.length == 0
+        assert opt.get("m").numel() == 0 and opt.get("v", 1).numel() == 0
+        assert opt.check_guards() == -1
+    norm, s = oa.GradNorm(xs).grad_norm(xs)
+    assert float(norm) == 0.0 and float(s) == 0.0
+
+
+def test_plans_on_two_streams_at_once(oa):
+    """Two plans step on streams of their own without waiting for each other."""
+    import torch
+    sizes = [300000, 5000, 1 << 21]
+    params, grads = make_inputs(sizes, 21, 1)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    opts, refs = [], []
+    dg = [dev(a) for a in grads[0]]
+    for k, s in enumerate(streams):
+        xs = [dev(a) for a in params]
+        torch.cuda.synchronize()
+        opts.append(oa.AdamW(xs, state_bits=(32, 8)[k], seed=k, stream=s))
+        refs.append(A.Reference(params, opts[k].offsets, (32, 8)[k], seed=k))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for opt, s in zip(opts, streams):
+            with torch.cuda.stream(s):
+                opt.step(dg, 1e-3, 0.1, max_norm=1.0)
+    torch.cuda.synchronize()
+    for ref in refs:
+        for t in range(6):
+            ref.step(grads[0], 1e-3, 0.1, 1.0)
+    view = opts[1].views()
+    for i, n in enumerate(sizes):
+        a = opts[1].offsets[i]
+        assert np.array_equal(view["v"][a:a + n].cpu().numpy(), refs[1].v[i][0])
+    assert_state(opts[0], refs[0], "32 bits")
+
+
+def test_rate_that_is_not_finite(oa):
+    """A NaN rate from the device makes every parameter NaN, whatever its
+    payload, stochastic rounding included."""
+    import torch
+    lr = torch.tensor([0x7FFFFFFF], dtype=torch.int32, device="cuda").view(torch.float32)
+    for bits in (32, 8):
+        x = torch.ones(3000, dtype=torch.bfloat16, device="cuda")
+        opt = oa.AdamW([x], state_bits=bits, stochastic=True)
+        opt.set("v", torch.full((3000,), 0.5, device="cuda"), 0)
+        opt.step([x.clone()], lr, 0.1)
+        assert bool(x.isnan().all())
+
+
 def test_state_round_trips_and_reads(oa):
     """set -> get: fp32 states come back as they are, 8-bit ones as the nearest
     codes' values, in fp32 and bfloat16, whole and by tensor."""
@@ -437,13 +504,14 @@ def test_checkpoint_resumes_bit_identically(oa):
             oa.AdamW(xs[:1], checkpoint=saved, **kw)
 
 
-def test_captured_steps_count_and_follow_the_device_rate(oa):
+@pytest.mark.parametrize("many", [False, True])
+def test_captured_steps_count_and_follow_the_device_rate(oa, many):
     """A captured clipped step, replayed between eager work: each replay is
     the next step (bias corrections and random bits included), at the rate
     that the device tensor holds then; two graphs of one plan on different
     gradients interleave."""
     import torch
-    sizes = [2000, 77, 4096]
+    sizes = [2000, 77, 4096] * (40 if many else 1)  # one launch, or several
     params, grads = make_inputs(sizes, 16, 2, "bf16", "bf16")
     for bits in (32, 8):
         side = torch.cuda.Stream()
