@@ -710,20 +710,31 @@ __global__ void __launch_bounds__(kBlock) control_kernel(Control* c, ControlArgs
 }
 
 // ---------------------------------------------------------- small launches --
+// Loads and stores past the caches, which each XCD has of its own: what one
+// block leaves here another finds, once the store is done.
+template <typename T>
+__device__ __forceinline__ T ld_shared_state(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void publish(double* p, double v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // done before what follows
+}
+
 // True for the last of `all` callers: each adds `one` (1) once, in one counter
 // where they are few, else over kLeaves of them whose last callers meet at a
 // root (a counter takes an atomic every 12 ns).  The counters are left at 0.
 // `id` numbers the callers from 0.
-template <int ORDER>
 __device__ __forceinline__ bool last_ticket(Control* c, uint32_t id, uint32_t all, uint32_t one) {
   const uint32_t leaves = all > 64 ? kLeaves : 1;
   const uint32_t leaf = id % leaves;
-  const uint32_t n = __hip_atomic_fetch_add(&c->leaf[leaf][0], one, ORDER,
+  const uint32_t n = __hip_atomic_fetch_add(&c->leaf[leaf][0], one, __ATOMIC_RELAXED,
                                             __HIP_MEMORY_SCOPE_AGENT);
   if (n != (all + leaves - 1 - leaf) / leaves - 1) return false;
   c->leaf[leaf][0] = 0;
   if (leaves == 1) return true;
-  if (__hip_atomic_fetch_add(&c->root, 1u, ORDER, __HIP_MEMORY_SCOPE_AGENT) != leaves - 1)
+  if (__hip_atomic_fetch_add(&c->root, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) !=
+      leaves - 1)
     return false;
   c->root = 0;
   return true;
@@ -734,11 +745,6 @@ __device__ __forceinline__ bool last_ticket(Control* c, uint32_t id, uint32_t al
 // the step while its row is being loaded, and takes a ticket once it has
 // them; the wave with the last ticket moves the counts on.  Nothing waits for
 // another wave.
-template <typename T>
-__device__ __forceinline__ T ld_shared_state(const T* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
 template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
 __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
   const ChunkRec rec = k.s.recs[blockIdx.x];
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
       // What is added depends on the loaded counts, so the ticket is taken
       // after they have arrived; none of them is ever negative.
       const uint32_t one = steps >= 0 && p1 >= 0.0 && p2 >= 0.0 ? 1u : 2u;
-      if (last_ticket<__ATOMIC_RELAXED>(ctl, blockIdx.x * (kBlock / 64) + wave,
+      if (last_ticket(ctl, blockIdx.x * (kBlock / 64) + wave,
                                         gridDim.x * (kBlock / 64), one)) {
         if (a.norm != nullptr) *a.norm = (float)d.norm;
         if (d.skip) {
@@ -793,8 +799,10 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
   step_wave<PT, GT, BITS, MASTER, SR>(g, p, k.s, rec.row, rec.state_row, wave, left, scalars);
 }
 
-// A chunk a block; the block with the last ticket, which each takes behind
-// its partial sum, folds the sums.
+// A chunk a block; the block with the last ticket, which each takes when its
+// partial sum has been stored, folds the sums.  At 256 chunks 4.4 us, 7.9 with
+// tickets that release and acquire (they write back and empty an L2 each), 6.1
+// with a kernel for the fold.
 template <typename GT>
 __global__ void __launch_bounds__(kBlock) small_norm_kernel(SmallNorm k) {
   __shared__ double red[kBlock / 64];
@@ -807,12 +815,14 @@ __global__ void __launch_bounds__(kBlock) small_norm_kernel(SmallNorm k) {
   const double acc = block_sum(row_sum(g + ((int64_t)rec.row + wave) * kRowElems + at, left, at),
                                red);
   if (threadIdx.x == 0) {
-    k.partials[blockIdx.x] = acc;
-    last = last_ticket<__ATOMIC_ACQ_REL>(k.control, blockIdx.x, gridDim.x, 1u);
+    publish(k.partials + blockIdx.x, acc);
+    last = last_ticket(k.control, blockIdx.x, gridDim.x, 1u);
   }
   __syncthreads();
   if (!last) return;
-  const double total = fold_partials(k.partials, gridDim.x, red);
+  static_assert(kSmallChunks <= kBlock, "a partial sum a thread");
+  const double total = block_sum(
+      threadIdx.x < gridDim.x ? ld_shared_state(k.partials + threadIdx.x) : 0.0, red);
   if (threadIdx.x != 0) return;
   if (k.sumsq != nullptr) *k.sumsq = total;
   if (k.norm != nullptr) *k.norm = (float)(sqrt(total) * (double)k.grad_scale);
@@ -871,7 +881,7 @@ __global__ void __launch_bounds__(kBlock)
 
 // `eights` runs of 8 elements from a multiple of 8 into a 16-byte aligned dst,
 // one a thread and round, all of a thread's loads ahead of its stores: 1.56B
-// codes to bfloat16 in 0.80 ms (5.8 TB/s; 0.89 ms with one run a round over a
+// codes to bfloat16 in 0.77 ms (6.0 TB/s; 0.89 ms with one run a round over a
 // grid of 8192 blocks).
 constexpr int kGetRounds = 4;
 constexpr int kGetElems = 8 * kBlock * kGetRounds;
