@@ -134,13 +134,14 @@ void fill_ptrs(const aw::Span& s, const void* const* params, const void* const* 
   }
 }
 
-// `fn(first chunk, chunks)` over a span, in launches of at most that size.
+// `fn(first chunk, chunks)` over a span, in equal launches of at most that size.
 template <typename F>
 hipError_t launches(ob_adamw_t h, const aw::Span& s, F fn) {
   const int64_t most = h->plan.cfg.state_bits == 32 ? kBlocks32 : kBlocks8;
+  const int64_t parts = (s.chunks + most - 1) / most, per = (s.chunks + parts - 1) / parts;
   hipError_t e = hipSuccess;
-  for (int64_t c = 0; c < s.chunks && e == hipSuccess; c += most)
-    e = fn(s.c0 + c, std::min(most, s.chunks - c));
+  for (int64_t c = 0; c < s.chunks && e == hipSuccess; c += per)
+    e = fn(s.c0 + c, std::min(per, s.chunks - c));
   return e;
 }
 

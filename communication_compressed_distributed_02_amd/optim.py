@@ -196,7 +196,8 @@ class AdamWOptimizer(torch.optim.Optimizer):
             if g is not None:
                 if g.is_sparse:
                     raise ValueError("sparse gradients are not supported")
-                g = g.detach().contiguous()
+                if not g.is_contiguous():
+                    g = g.contiguous()
             out.append(g)
         return out
 
@@ -214,7 +215,7 @@ class AdamWOptimizer(torch.optim.Optimizer):
             lr = [float(g["lr"]) for g in self.param_groups]
         grads = self.grads()
         # the parameters as they lie now
-        batch = self._core.bind(grads, [p.detach() for p in self.params])
+        batch = self._core.bind(grads, self.params)
         self.norm = self._core.step(batch, lr, [g["weight_decay"] for g in self.param_groups],
                                     self.max_norm, grad_scale, self.skip_nonfinite, sumsq)
         torch.autograd.graph.increment_version(
