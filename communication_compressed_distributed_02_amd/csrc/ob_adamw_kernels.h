@@ -73,7 +73,8 @@ struct SmallNorm {
   float grad_scale;
   const void* g[kSmallTensors];
 };
-static_assert(sizeof(SmallStep) <= 4096 && sizeof(StepPtrs) + sizeof(State) + 16 <= 4096,
+static_assert(sizeof(SmallStep) <= 4096 && sizeof(StepPtrs) + sizeof(State) + 16 <= 4096 &&
+                  sizeof(NormPtrs) + 48 <= 4096,
               "kernel arguments");
 
 // A step of n <= kSmallChunks chunks: control and update in one launch.

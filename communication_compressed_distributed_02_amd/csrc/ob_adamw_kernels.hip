@@ -197,7 +197,8 @@ __device__ __forceinline__ uint32_t encode_v(f32x4 v, uint32_t* e_out, N noise) 
   uint32_t q[4], top = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    q[k] = (__float_as_uint(v[k]) + noise(k)) >> 20;
+    // without the sign, so that no NaN's pattern wraps around to a small one
+    q[k] = ((__float_as_uint(v[k]) & 0x7fffffffu) + noise(k)) >> 20;
     top = umax(top, q[k]);
   }
   top = wave_max(top);
@@ -418,7 +419,8 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
     } else {
       const uint32_t em = (me >> (8 * u)) & 255u, ev = (ve >> (8 * u)) & 255u;
       // No code of v is special and m's scale times b1 is a normal number:
-      // then v stays above zero and decoding needs no exceptions.
+      // then v stays above zero and decoding needs no exceptions.  (A v that
+      // is not finite comes from such a gradient, and so with such an m.)
       bool plain = plain_scalars && em >= 16u && __ballot(special_codes(vc[u])) == 0;
       if (plain) {
         // b1 * (code * 2^k) rounds as (b1 * 2^k) * code does
@@ -778,8 +780,7 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
       // What is added depends on the loaded counts, so the ticket is taken
       // after they have arrived; none of them is ever negative.
       const uint32_t one = steps >= 0 && p1 >= 0.0 && p2 >= 0.0 ? 1u : 2u;
-      if (last_ticket(ctl, blockIdx.x * (kBlock / 64) + wave,
-                                        gridDim.x * (kBlock / 64), one)) {
+      if (last_ticket(ctl, blockIdx.x * (kBlock / 64) + wave, gridDim.x * (kBlock / 64), one)) {
         if (a.norm != nullptr) *a.norm = (float)d.norm;
         if (d.skip) {
           ctl->skipped += 1;

@@ -292,6 +292,29 @@ def test_nonfinite_and_huge_elements_stay_where_they_are(oa):
         assert np.isnan(ref.x[0][3]) and np.isfinite(ref.x[0][4])
 
 
+def test_nan_of_any_payload_is_held_as_nan(oa):
+    """Gradients whose NaN patterns are the least, the greatest and negative,
+    alone in a group of 8-bit codes, in a step that starts from zeros and in a
+    later one."""
+    import torch
+    n = 6 * 256
+    patterns = [0x7F800001, 0x7FC00000, 0x7FFFFFFF, 0xFF800001, 0xFFC00000, 0xFFFFFFFF]
+    for warm in (0, 2):
+        x = torch.zeros(n, device="cuda")
+        opt = oa.AdamW([x], state_bits=8)
+        g = torch.full((n,), 0.5, device="cuda")
+        for _ in range(warm):
+            opt.step([g], 1e-3)
+        bits = g.view(torch.int32)
+        for i, b in enumerate(patterns):
+            bits[256 * i + 17] = b - (1 << 32) if b >> 31 else b
+        opt.step([g], 1e-3)
+        bad = np.arange(n) % 256 == 17
+        for got in (host(x), host(opt.get("m")[:n]), host(opt.get("v")[:n])):
+            assert np.array_equal(np.isnan(got), bad), warm
+        assert (opt.views()["v"][:n].cpu().numpy()[bad] == 255).all()
+
+
 def test_clipping_by_a_nonfinite_norm(oa):
     """An infinite norm scales every finite gradient to zero, a NaN one makes
     every gradient NaN; what lies between tensors stays zero."""
