@@ -201,6 +201,9 @@ class _Plan(OnStream):
             if checkpoint is not None and checkpoint.numel() != self.ws_bytes:
                 raise ValueError("checkpoint of %d bytes, workspace needs %d"
                                  % (checkpoint.numel(), self.ws_bytes))
+            # what results are made like: a third less time than naming a type and device
+            self._like_norm = torch.empty((), dtype=torch.float32, device=self.device)
+            self._like_sumsq = torch.empty((), dtype=torch.float64, device=self.device)
             self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             self._order_after_caller(self.workspace)
             if checkpoint is not None:
@@ -213,14 +216,14 @@ class _Plan(OnStream):
                 self.h = ob_adamw_init(cfg, self.numels, self.groups, self.workspace.data_ptr(),
                                        self.ws_bytes, params, self.stream.cuda_stream)
 
-    def _call(self, tensors, fn, *args):
+    def _call(self, lists, fn, *args):
         """fn(*args) with this plan's device current, ordered with the
-        caller's stream.  On a stream under capture the call is recorded there
-        (the plan's own stream may be the default one, which cannot take part
-        in a capture)."""
+        caller's stream; lists: of the tensors it touches.  On a stream under
+        capture the call is recorded there (the plan's own stream may be the
+        default one, which cannot take part in a capture)."""
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                self._call(tensors, fn, *args)
+                self._call(lists, fn, *args)
             return
         current = _current_stream(self.device.index)
         if current == self._stream_ptr:
@@ -232,7 +235,7 @@ class _Plan(OnStream):
             finally:
                 ob_adamw_set_stream(self.h, self._stream_ptr)
         else:
-            self._ordered(tensors, fn, *args)
+            self._ordered([t for some in lists for t in some], fn, *args)
 
     def _ptrs(self, tensors, dtype, what, may_lack):
         if len(tensors) != len(self.numels):
@@ -257,9 +260,8 @@ class _Plan(OnStream):
             self, tuple(grads), self._ptrs(grads, self.grad_dtype, "gradients", True), (), None)
         if b.plan is not self:
             raise ValueError("a batch bound by another plan")
-        norm = torch.empty((), dtype=torch.float32, device=self.device)
-        sumsq = torch.empty((), dtype=torch.float64, device=self.device)
-        self._call((norm, sumsq) + b.tensors, ob_adamw_grad_norm, self.h, b.grad_ptrs, grad_scale,
+        norm, sumsq = torch.empty_like(self._like_norm), torch.empty_like(self._like_sumsq)
+        self._call((b.tensors, (norm, sumsq)), ob_adamw_grad_norm, self.h, b.grad_ptrs, grad_scale,
                    sumsq.data_ptr(), norm.data_ptr())
         return norm, sumsq
 
@@ -378,14 +380,14 @@ class AdamW(_Plan):
         b = grads if isinstance(grads, TensorBatch) else self.bind(grads)
         if b.plan is not self:
             raise ValueError("a batch bound by another plan")
-        a, tensors = self._args, b.tensors
+        a, more = self._args, []
         if isinstance(lr, torch.Tensor):
             if (lr.dtype != torch.float32 or lr.numel() != self.n_groups
                     or lr.device != self.device or not lr.is_contiguous()):
                 raise ValueError("lr must be a contiguous float32 tensor of %d elements on %s"
                                  % (self.n_groups, self.device))
             a.lr_device = lr.data_ptr()
-            tensors = tensors + (lr,)
+            more.append(lr)
         else:
             a.lr_device = None
             self._per_group(lr, self._lr, "learning rates")
@@ -396,17 +398,17 @@ class AdamW(_Plan):
                     or sumsq.device != self.device):
                 raise ValueError("sumsq must be a float64 scalar on %s" % self.device)
             a.sumsq = sumsq.data_ptr()
-            tensors = tensors + (sumsq,)
+            more.append(sumsq)
         else:
             a.sumsq = None
         norm = None
         if max_norm or skip_nonfinite:
-            norm = torch.empty((), dtype=torch.float32, device=self.device)
+            norm = torch.empty_like(self._like_norm)
             a.norm = norm.data_ptr()
-            tensors = tensors + (norm,)
+            more.append(norm)
         else:
             a.norm = None
-        self._call(tensors, ob_adamw_step, self.h, b.param_ptrs, b.grad_ptrs, self._args_ref)
+        self._call((b.tensors, more), ob_adamw_step, self.h, b.param_ptrs, b.grad_ptrs, self._args_ref)
         return norm
 
     def views(self):
@@ -434,7 +436,7 @@ class AdamW(_Plan):
         offset, count = (0, self.length) if tensor is None else (self.offsets[tensor],
                                                                  self.numels[tensor])
         out = torch.empty(count, dtype=dtype, device=self.device)
-        self._call((out,), ob_adamw_get_state, self.h, FIELDS[name], offset, count, _TYPES[dtype],
+        self._call(((out,),), ob_adamw_get_state, self.h, FIELDS[name], offset, count, _TYPES[dtype],
                    out.data_ptr() if count else None)
         return out
 
@@ -448,7 +450,7 @@ class AdamW(_Plan):
         rows = -(-n // 1024) * 1024
         whole = torch.zeros(rows, dtype=torch.float32, device=self.device)
         whole[:n].copy_(src.reshape(-1))
-        self._call((whole,), ob_adamw_set_state, self.h, FIELDS[name], self.offsets[tensor], rows,
+        self._call(((whole,),), ob_adamw_set_state, self.h, FIELDS[name], self.offsets[tensor], rows,
                    whole.data_ptr() if n else None)
 
     def set_steps(self, steps):
