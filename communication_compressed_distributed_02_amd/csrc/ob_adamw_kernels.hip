@@ -152,25 +152,30 @@ __device__ __forceinline__ uint32_t codes_m(f32x4 m, uint32_t e) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(m.z * s, m.w * s, c, true);
 }
 
-// Codes and exponent of a group whose elements lane by lane are m.
-__device__ __forceinline__ uint32_t encode_m(f32x4 m, uint32_t* e_out) {
-  uint32_t a[4], top = 0;
+// The wave's largest |m|, as a pattern.
+__device__ __forceinline__ uint32_t top_m(f32x4 m) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    a[k] = __float_as_uint(m[k]) & 0x7fffffffu;
-    top = umax(top, a[k]);
-  }
-  uint32_t e = wave_max(top) >> 23;
-  if (e == 255u) {  // something is not finite: held as NaN, the others keep their scale
-    top = 0;
+  for (int k = 0; k < 4; ++k) top = umax(top, __float_as_uint(m[k]) & 0x7fffffffu);
+  return wave_max(top);
+}
+
+// Codes and exponent of a group whose elements lane by lane are m, top =
+// top_m(m).
+__device__ __forceinline__ uint32_t encode_m(f32x4 m, uint32_t top, uint32_t* e_out) {
+  if (top >= 0x7f800000u) {  // something is not finite: held as NaN, the others keep their scale
+    f32x4 rest = m;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (finite_bits(a[k])) top = umax(top, a[k]);
-      else m[k] = __uint_as_float(0x7fc00000u);
+      if (!finite_bits(__float_as_uint(m[k]))) {
+        rest[k] = 0.0f;
+        m[k] = __uint_as_float(0x7fc00000u);
+      }
     }
-    e = wave_max(top) >> 23;
+    top = top_m(rest);
   }
-  *e_out = e = umax(e, (uint32_t)kMinExpM);
+  const uint32_t e = umax(top >> 23, (uint32_t)kMinExpM);
+  *e_out = e;
   return codes_m(m, e);
 }
 
@@ -191,17 +196,20 @@ __device__ __forceinline__ f32x4 decode_v(uint32_t codes, uint32_t e) {
   return v;
 }
 
-// noise(k): what is added to element k's pattern before its low 20 bits go.
-template <typename N>
-__device__ __forceinline__ uint32_t encode_v(f32x4 v, uint32_t* e_out, N noise) {
-  uint32_t q[4], top = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    // without the sign, so that no NaN's pattern wraps around to a small one
-    q[k] = ((__float_as_uint(v[k]) & 0x7fffffffu) + noise(k)) >> 20;
-    top = umax(top, q[k]);
-  }
-  top = wave_max(top);
+// A v's pattern with `noise` added, less its low 20 bits: rounded to the codes'
+// steps.  The sign goes, so that no NaN's pattern wraps around to a small one.
+__device__ __forceinline__ uint32_t rounded_v(float v, uint32_t noise) {
+  return ((__float_as_uint(v) & 0x7fffffffu) + noise) >> 20;
+}
+// 16 random bits as that noise, half a unit up: no bias.
+__device__ __forceinline__ uint32_t noise_v(uint32_t a, uint32_t b, int k) {
+  return (random16(a, b, k) << 4) | 8u;
+}
+
+// Codes and exponent of a group whose elements lane by lane are v, rounded to
+// q, top the wave's largest q.
+__device__ __forceinline__ uint32_t encode_v(f32x4 v, uint32_t (&q)[4], uint32_t top,
+                                             uint32_t* e_out) {
   uint32_t odd = 0;  // bit k: element k is not finite
   if (top >= 2040u) {  // something is not finite, or the largest fp32 values round up to infinity
     top = 0;
@@ -371,6 +379,7 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) {
     const int o = u * kScaleElems, n = left - o - at;
+    if (!WHOLE && o >= left) break;  // groups behind the tensor's last element
     gq[u].load(g + o, n);
     if constexpr (MASTER) xm[u] = load4(master + o);
     else pq[u].load(p + o, n);
@@ -396,6 +405,11 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) {
     const int o = u * kScaleElems, n = left - o - at;
+    if (!WHOLE && o >= left) {  // they hold zeros and keep them
+      new_me |= (uint32_t)kMinExpM << (8 * u);
+      new_ve |= (uint32_t)kMinExpV << (8 * u);
+      continue;
+    }
     const f32x4 gv = gq[u].values() * c.gs;
     f32x4 x, m, v;
     if constexpr (MASTER) x = xm[u];
@@ -436,7 +450,7 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
         m = decode_m(mc[u], em) * b1;
         v = decode_v(vc[u], ev);
       }
-      uint32_t q[4], tm = 0, tv = 0;
+      uint32_t q[4], tv = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         m[k] = m[k] + (ob1 * gv[k]);
@@ -448,11 +462,10 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        q[k] = (__float_as_uint(v[k]) + ((random16(w.w[0], w.w[1], k) << 4) | 8u)) >> 20;
-        tm = umax(tm, __float_as_uint(m[k]) & 0x7fffffffu);
+        q[k] = rounded_v(v[k], noise_v(w.w[0], w.w[1], k));
         tv = umax(tv, q[k]);
       }
-      tm = wave_max(tm);
+      const uint32_t tm = top_m(m);
       tv = wave_max(tv);
       uint32_t cm, cv, e;
       if (plain && tm < (217u << 23) && tv < (227u << 3) && WHOLE) {
@@ -477,9 +490,9 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
           x[k] = updated(x[k], m[k], v[k], c.decay, c.rate, c.rbc2, s.eps);
         if constexpr (!WHOLE) clear_behind(n, m, v, x);
         put<SR, true, WHOLE>(p + o, x, n, w);
-        cm = encode_m(m, &e);
+        cm = encode_m(m, tm, &e);
         new_me |= e << (8 * u);
-        cv = encode_v(v, &e, [&](int k) { return (random16(w.w[0], w.w[1], k) << 4) | 8u; });
+        cv = encode_v(v, q, tv, &e);
         new_ve |= e << (8 * u);
       }
       st_stream((uint32_t*)(m8 + o), cm);
@@ -938,11 +951,16 @@ __global__ void __launch_bounds__(kBlock)
     f32x4 x = load_some(src + i * kScaleElems + lane * 4, 4);
     uint32_t e, c;
     if constexpr (FIELD == OB_ADAMW_M) {
-      c = encode_m(x, &e);
+      c = encode_m(x, top_m(x), &e);
     } else {
+      uint32_t q[4], top = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = x[k] <= 0.0f ? 0.0f : x[k];  // NaN stays
-      c = encode_v(x, &e, [](int) { return 1u << 19; });
+      for (int k = 0; k < 4; ++k) {
+        x[k] = x[k] <= 0.0f ? 0.0f : x[k];  // NaN stays
+        q[k] = rounded_v(x[k], 1u << 19);   // to nearest
+        top = umax(top, q[k]);
+      }
+      c = encode_v(x, q, wave_max(top), &e);
     }
     const int64_t at = group0 + i;
     ((uint32_t*)(FIELD == OB_ADAMW_M ? s.m : s.v))[at * 64 + lane] = c;
