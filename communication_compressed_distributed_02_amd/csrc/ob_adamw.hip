@@ -19,12 +19,11 @@ namespace {
 namespace aw = ob::adamw;
 
 constexpr int64_t kMaxSteps = (int64_t(1) << 31) - 1;
-// Blocks of one launch of the step, 1.3 to 2 GB of traffic.  With 32-bit
-// states one launch over everything runs 3 to 5 % slower than launches of
-// 2^14 blocks (334M parameters 1588 and 1543 us, 1.56B 8.19 and 7.72 ms);
-// with 8-bit ones 2^15 is as fast as anything larger, and 2^14 2 % slower
-// (1.56B 3.13 and 3.18 ms).  Far below the 2^32 threads a grid can hold.
-constexpr int64_t kBlocks32 = int64_t(1) << 14, kBlocks8 = int64_t(1) << 15;
+// Chunks of one launch of the step, 2 to 4 GB of traffic.  32-bit states,
+// 2^14, 2^15 and 2^17 chunks: 1458, 1487 and 1507 us on 334M parameters, 7.62,
+// 7.70 and 7.91 ms on 1.56B; 2^13 as 2^14.  8-bit ones, 2^14, 2^15, 2^16 and
+// 2^18: 1072, 1074, 1078 and 1079 us, 3.11, 3.05, 3.01 and 3.02 ms.
+constexpr int64_t kChunks32 = int64_t(1) << 14, kChunks8 = int64_t(1) << 16;
 static_assert(aw::kGuardGap == ob::kGuardBytes, "the guards are those of ob_adam workspaces");
 
 }  // namespace
@@ -137,7 +136,7 @@ void fill_ptrs(const aw::Span& s, const void* const* params, const void* const* 
 // `fn(first chunk, chunks)` over a span, in equal launches of at most that size.
 template <typename F>
 hipError_t launches(ob_adamw_t h, const aw::Span& s, F fn) {
-  const int64_t most = h->plan.cfg.state_bits == 32 ? kBlocks32 : kBlocks8;
+  const int64_t most = h->plan.cfg.state_bits == 32 ? kChunks32 : kChunks8;
   const int64_t parts = (s.chunks + most - 1) / most, per = (s.chunks + parts - 1) / parts;
   hipError_t e = hipSuccess;
   for (int64_t c = 0; c < s.chunks && e == hipSuccess; c += per)

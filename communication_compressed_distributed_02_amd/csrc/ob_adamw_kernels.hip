@@ -1,12 +1,13 @@
 // gfx950 kernels of AdamW's step over many tensors and of the gradient norm.
 // The arithmetic contract is stated in include/ob_adamw.h.
 //
-// Mapping: a block of 4 waves owns a chunk of 4096 elements of one tensor, a
-// wave a row of 1024 of them, and a lane 4 consecutive elements of each of
-// the row's 4 groups of 256.  A group is the unit that shares the exponents of
-// an 8-bit state, so its maximum is a reduction over one wave's lanes, in
-// registers.  The list of chunks (tensor, place, length, group) is made once
-// per plan; the tensors' pointers come by value with each launch.
+// Mapping: work is listed in chunks of 4096 elements of one tensor, made of 16
+// groups of 256, of which a lane takes 4 consecutive elements.  A group is the
+// unit that shares the exponents of an 8-bit state, so its maximum is a
+// reduction over one wave's lanes, in registers.  A wave takes 4 groups of the
+// norm, and 1 or 2 of the step (kStepGroups).  The list of chunks (tensor,
+// place, length, hyperparameter group) is made once per plan; the tensors'
+// pointers come by value with each launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -26,7 +27,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int64_t kKeptBytes = int64_t(240) << 20;  // gradients that a norm leaves in the caches
 
-constexpr int kGroups = kRowElems / kScaleElems;  // groups of 256 in a wave's row
+constexpr int kGroups = kRowElems / kScaleElems;  // groups of 256 in a row of 1024
 
 struct bf16 {
   uint16_t bits;
@@ -56,9 +57,11 @@ __device__ __forceinline__ void st_stream(T* p, T v) { __builtin_nontemporal_sto
 // that its accesses straddle and no other code.
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
-__device__ __forceinline__ f32x4 load4(const float* p) { return ld_stream((const f32x4_at4*)p); }
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  return __builtin_nontemporal_load((const f32x4_at4*)p);
+}
 __device__ __forceinline__ u32x2 load_packed(const bf16* p) {
-  return ld_stream((const u32x2_at2*)p);
+  return __builtin_nontemporal_load((const u32x2_at2*)p);
 }
 // The same, left in the caches.
 __device__ __forceinline__ f32x4 load4_kept(const float* p) { return *(const f32x4_at4*)p; }
@@ -292,7 +295,7 @@ struct Quad<bf16, true> {
 template <bool WHOLE>
 __device__ __forceinline__ void store_param(float* p, f32x4 x, int n) {
   if constexpr (WHOLE) {
-    st_stream((f32x4_at4*)p, f32x4_at4(x));
+    __builtin_nontemporal_store(x, (f32x4_at4*)p);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -302,7 +305,7 @@ __device__ __forceinline__ void store_param(float* p, f32x4 x, int n) {
 template <bool WHOLE>
 __device__ __forceinline__ void store_param(bf16* p, u32x2 w, int n) {
   if constexpr (WHOLE) {
-    st_stream((u32x2_at2*)p, u32x2_at2(w));
+    __builtin_nontemporal_store(w, (u32x2_at2*)p);
   } else {
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -358,26 +361,33 @@ __device__ __forceinline__ uint32_t special_codes(uint32_t c) {
   return ((low & ~c) | (high & c)) & 0x80808080u;
 }
 
-// One row of 1024 elements of one tensor.  WHOLE: all of them are the tensor's.
-// scalars() is called when the row's loads are under way.
-template <typename PT, typename GT, int BITS, bool MASTER, bool SR, bool WHOLE, typename F>
-__device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int64_t srow,
-                                         int left, F scalars) {
+// The exponent bytes of a wave's groups, as one value.
+template <int GROUPS>
+using exps_t = std::conditional_t<GROUPS == 1, uint8_t,
+                                  std::conditional_t<GROUPS == 2, uint16_t, uint32_t>>;
+
+// GROUPS groups of 256 elements of one tensor, whose state starts at element
+// 256*group.  WHOLE: all of them are the tensor's.  scalars() is called when
+// the loads are under way.
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR, int GROUPS, bool WHOLE,
+          typename F>
+__device__ __forceinline__ void step_groups(const GT* g, PT* p, const State& s, int64_t group,
+                                            int left, F scalars) {
   const int lane = threadIdx.x & 63;
   const int at = lane * 4;
-  float* master = s.master + srow * kRowElems + at;
-  float* m32 = (float*)s.m + srow * kRowElems + at;
-  float* v32 = (float*)s.v + srow * kRowElems + at;
-  uint8_t* m8 = (uint8_t*)s.m + srow * kRowElems + at;
-  uint8_t* v8 = (uint8_t*)s.v + srow * kRowElems + at;
+  float* master = s.master + group * kScaleElems + at;
+  float* m32 = (float*)s.m + group * kScaleElems + at;
+  float* v32 = (float*)s.v + group * kScaleElems + at;
+  uint8_t* m8 = (uint8_t*)s.m + group * kScaleElems + at;
+  uint8_t* v8 = (uint8_t*)s.v + group * kScaleElems + at;
   g += at;
   p += at;
-  Quad<GT, WHOLE> gq[kGroups];
-  Quad<PT, WHOLE> pq[kGroups];
-  f32x4 xm[kGroups], mv[kGroups], vv[kGroups];
-  uint32_t mc[kGroups], vc[kGroups], me = 0, ve = 0;
+  Quad<GT, WHOLE> gq[GROUPS];
+  Quad<PT, WHOLE> pq[GROUPS];
+  f32x4 xm[GROUPS], mv[GROUPS], vv[GROUPS];
+  uint32_t mc[GROUPS], vc[GROUPS], me = 0, ve = 0;
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) {
+  for (int u = 0; u < GROUPS; ++u) {
     const int o = u * kScaleElems, n = left - o - at;
     if (!WHOLE && o >= left) break;  // groups behind the tensor's last element
     gq[u].load(g + o, n);
@@ -392,18 +402,18 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
     }
   }
   if constexpr (BITS == 8) {
-    me = *(const uint32_t*)(s.m_exp + srow * kGroups);
-    ve = *(const uint32_t*)(s.v_exp + srow * kGroups);
+    me = *(const exps_t<GROUPS>*)(s.m_exp + group);
+    ve = *(const exps_t<GROUPS>*)(s.v_exp + group);
   }
   const Scalars c = scalars();
   if (c.skip) return;
   const float b1 = s.beta1, ob1 = 1.0f - b1, b2 = s.beta2, ob2 = 1.0f - b2;
-  const uint64_t quad0 = (uint64_t)srow * (kRowElems / 4);
+  const uint64_t quad0 = (uint64_t)group * (kScaleElems / 4);
   const uint32_t key0 = high_key(quad0, c.key0), key1 = c.key1;
   const bool plain_scalars = s.eps >= 0x1p-30f && b2 >= 0x1p-10f;
   uint32_t new_me = 0, new_ve = 0;
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) {
+  for (int u = 0; u < GROUPS; ++u) {
     const int o = u * kScaleElems, n = left - o - at;
     if (!WHOLE && o >= left) {  // they hold zeros and keep them
       new_me |= (uint32_t)kMinExpM << (8 * u);
@@ -502,41 +512,54 @@ __device__ __forceinline__ void step_row(const GT* g, PT* p, const State& s, int
   }
   if constexpr (BITS == 8) {
     if (lane == 0) {
-      *(uint32_t*)(s.m_exp + srow * kGroups) = new_me;
-      *(uint32_t*)(s.v_exp + srow * kGroups) = new_ve;
+      *(exps_t<GROUPS>*)(s.m_exp + group) = (exps_t<GROUPS>)new_me;
+      *(exps_t<GROUPS>*)(s.v_exp + group) = (exps_t<GROUPS>)new_ve;
     }
   }
 }
 
-// This wave's row of a chunk: rows of one block are the chunk's four.
-template <typename PT, typename GT, int BITS, bool MASTER, bool SR, typename F>
-__device__ __forceinline__ void step_wave(const GT* g, PT* p, const State& s, uint32_t row0,
-                                          uint32_t state_row, int wave, int left, F scalars) {
-  const int64_t row = (int64_t)row0 + wave;
-  const int64_t srow = (int64_t)state_row + wave;
-  g += row * kRowElems;
-  p += row * kRowElems;
-  if (left >= kRowElems)
-    step_row<PT, GT, BITS, MASTER, SR, true>(g, p, s, srow, left, scalars);
+// This wave's share of a chunk, from its element `begin` on: `left` elements, of
+// which it takes GROUPS groups.
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR, int GROUPS, typename F>
+__device__ __forceinline__ void step_wave(const GT* g, PT* p, const State& s, uint32_t row,
+                                          uint32_t state_row, int begin, int left, F scalars) {
+  const int64_t group = (int64_t)state_row * kGroups + begin / kScaleElems;
+  g += (int64_t)row * kRowElems + begin;
+  p += (int64_t)row * kRowElems + begin;
+  if (left >= GROUPS * kScaleElems)
+    step_groups<PT, GT, BITS, MASTER, SR, GROUPS, true>(g, p, s, group, left, scalars);
   else
-    step_row<PT, GT, BITS, MASTER, SR, false>(g, p, s, srow, left, scalars);
+    step_groups<PT, GT, BITS, MASTER, SR, GROUPS, false>(g, p, s, group, left, scalars);
 }
+
+// Groups that a wave of a step over many chunks takes, and blocks of a chunk.
+// 32-bit states, 1, 2 and 4 groups: 1458, 1480 and 1505 us on 334M parameters in
+// 390 tensors, 73, 74 and 77 on 13M in 61.  8-bit ones: 39.8, 38.3 and 41.2 on
+// the 61, 3.43, 3.00 and 2.98 ms on 1.56B (the scalars' share of a wave's
+// instructions).
+template <int BITS>
+constexpr int kStepGroups = BITS == 32 ? 1 : 2;
+template <int BITS>
+constexpr int kStepBlocks = kGroups / kStepGroups<BITS>;
 
 template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
 __global__ void __launch_bounds__(kBlock)
     step_kernel(StepPtrs ptrs, State s, uint32_t t0, int64_t c0) {
+  constexpr int kShare = kStepGroups<BITS> * kScaleElems;  // of a wave
   const Control* __restrict__ ctl = s.control;
-  const ChunkRec rec = s.recs[c0 + blockIdx.x];
+  const ChunkRec rec = s.recs[c0 + blockIdx.x / kStepBlocks<BITS>];
   const GT* g = (const GT*)ptrs.g[rec.tensor - t0];
   PT* p = (PT*)ptrs.p[rec.tensor - t0];
   if (g == nullptr || ctl->skip) return;
-  const int wave = wave_in_block();
-  const int left = (int)rec.count - wave * kRowElems;  // elements from this wave's row on
+  const int begin =
+      ((int)(blockIdx.x % kStepBlocks<BITS>) * (kBlock / 64) + wave_in_block()) * kShare;
+  const int left = (int)rec.count - begin;
   if (left <= 0) return;
-  step_wave<PT, GT, BITS, MASTER, SR>(g, p, s, rec.row, rec.state_row, wave, left, [&] {
-    return Scalars{ctl->gscale, ctl->decay[rec.group], ctl->rate[rec.group], ctl->rbc2,
-                   ctl->k0,     ctl->k1,               false};
-  });
+  step_wave<PT, GT, BITS, MASTER, SR, kStepGroups<BITS>>(
+      g, p, s, rec.row, rec.state_row, begin, left, [&] {
+        return Scalars{ctl->gscale, ctl->decay[rec.group], ctl->rate[rec.group], ctl->rbc2,
+                       ctl->k0,     ctl->k1,               false};
+      });
 }
 
 // ------------------------------------------------------------------ norm --
@@ -760,16 +783,19 @@ __device__ __forceinline__ bool last_ticket(Control* c, uint32_t id, uint32_t al
 // the step while its row is being loaded, and takes a ticket once it has
 // them; the wave with the last ticket moves the counts on.  Nothing waits for
 // another wave.
-template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
+template <typename PT, typename GT, int BITS, bool MASTER, bool SR, int GROUPS>
 __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
-  const ChunkRec rec = k.s.recs[blockIdx.x];
+  constexpr int kShare = GROUPS * kScaleElems;             // of a wave
+  constexpr int kWaves = kChunkElems / kShare;             // of a chunk
+  const int id = blockIdx.x * (kBlock / 64) + wave_in_block();
+  const ChunkRec rec = k.s.recs[id / kWaves];
   const GT* g = (const GT*)k.g[rec.tensor];
   PT* p = (PT*)k.p[rec.tensor];
   const ControlArgs& a = k.a;
   Control* ctl = k.s.control;
   const int lane = threadIdx.x & 63;
-  const int wave = wave_in_block();
-  const int left = (int)rec.count - wave * kRowElems;
+  const int begin = id % kWaves * kShare;
+  const int left = (int)rec.count - begin;
   const int64_t steps = ld_shared_state(&ctl->steps);
   const double p1 = ld_shared_state(&ctl->p1), p2 = ld_shared_state(&ctl->p2);
   double part = 0.0;
@@ -793,7 +819,7 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
       // What is added depends on the loaded counts, so the ticket is taken
       // after they have arrived; none of them is ever negative.
       const uint32_t one = steps >= 0 && p1 >= 0.0 && p2 >= 0.0 ? 1u : 2u;
-      if (last_ticket(ctl, blockIdx.x * (kBlock / 64) + wave, gridDim.x * (kBlock / 64), one)) {
+      if (last_ticket(ctl, id, gridDim.x * (kBlock / 64), one)) {
         if (a.norm != nullptr) *a.norm = (float)d.norm;
         if (d.skip) {
           ctl->skipped += 1;
@@ -810,7 +836,8 @@ __global__ void __launch_bounds__(kBlock) small_step_kernel(SmallStep k) {
     scalars();
     return;
   }
-  step_wave<PT, GT, BITS, MASTER, SR>(g, p, k.s, rec.row, rec.state_row, wave, left, scalars);
+  step_wave<PT, GT, BITS, MASTER, SR, GROUPS>(g, p, k.s, rec.row, rec.state_row, begin, left,
+                                              scalars);
 }
 
 // A chunk a block; the block with the last ticket, which each takes when its
@@ -983,15 +1010,25 @@ int grid_for(int64_t threads) {
   return (int)(blocks < 1 ? 1 : (blocks > 8192 ? 8192 : blocks));
 }
 
+// A wave takes one group where a step has so few chunks, four else: the latency
+// of one wave's instructions shows.  8-bit states, 16 chunks 4.8 and 6.2 us, 64
+// chunks 6.0 and 6.3, 128 chunks 7.2 and 6.4 (four times the tickets).
+constexpr int64_t kFewChunks = 64;
+
 // fn(types and kinds of the plan's step as compile-time values).
 template <typename PT, typename GT, int BITS, bool MASTER, bool SR>
 struct Kind {
   static void step(const StepPtrs& ptrs, const State& s, uint32_t t0, int64_t c0, int64_t n,
                    hipStream_t stream) {
-    step_kernel<PT, GT, BITS, MASTER, SR><<<(unsigned)n, kBlock, 0, stream>>>(ptrs, s, t0, c0);
+    step_kernel<PT, GT, BITS, MASTER, SR>
+        <<<(unsigned)n * kStepBlocks<BITS>, kBlock, 0, stream>>>(ptrs, s, t0, c0);
   }
   static void small(const SmallStep& k, int64_t n, hipStream_t stream) {
-    small_step_kernel<PT, GT, BITS, MASTER, SR><<<(unsigned)n, kBlock, 0, stream>>>(k);
+    if (n <= kFewChunks)
+      small_step_kernel<PT, GT, BITS, MASTER, SR, 1>
+          <<<(unsigned)n * kGroups, kBlock, 0, stream>>>(k);
+    else
+      small_step_kernel<PT, GT, BITS, MASTER, SR, kGroups><<<(unsigned)n, kBlock, 0, stream>>>(k);
   }
 };
 template <typename PT, typename GT, int BITS, typename F>

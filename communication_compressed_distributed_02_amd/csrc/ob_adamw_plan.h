@@ -16,8 +16,8 @@ namespace ob {
 namespace adamw {
 
 constexpr int kBlock = 256;         // threads of a block: 4 waves
-constexpr int kRowElems = 1024;     // a wave's share; a tensor's state starts at a multiple of it
-constexpr int kChunkElems = 4 * kRowElems;  // a block's share of one tensor
+constexpr int kRowElems = 1024;     // a tensor's state starts at a multiple of it
+constexpr int kChunkElems = 4 * kRowElems;  // a record's share of one tensor
 constexpr int kScaleElems = 256;    // elements that share the exponents of an 8-bit state
 constexpr int kMaxGroups = OB_ADAMW_MAX_GROUPS;
 // Pointers travel by value in the kernel arguments (4 KB of them), so a
@@ -27,8 +27,8 @@ constexpr int kPtrsPerNorm = 480;
 constexpr int kNormBlocks = 2048;   // partial sums of one launch of the norm, at most
 // A step over at most so many chunks (2^20 elements) and tensors is one launch
 // without a control kernel in front, and a norm over them one without a
-// kernel behind.  32-bit states: 5.3 and 7.0 us at 8 chunks, 7.2 and 8.6 at
-// 256, 20.8 and 22.2 at 1024; 8-bit ones, clipped: 11.8 and 12.9 at 256, 14.6
+// kernel behind.  32-bit states: 4.8 and 7.0 us at 8 chunks, 7.4 and 8.6 at
+// 256, 20.8 and 22.2 at 1024; 8-bit ones, clipped: 11.0 and 12.9 at 256, 14.6
 // and 13.4 at 512.
 constexpr int kSmallChunks = 256;
 constexpr int kSmallTensors = 96;
@@ -38,7 +38,7 @@ constexpr int64_t kMaxLength = int64_t(1) << 40;  // of a state array; no size b
 constexpr int kNumGuards = 8;
 constexpr uint64_t kGuardGap = 256;
 
-// One block's work: `count` elements of tensor `tensor` from its element
+// One chunk of work: `count` elements of tensor `tensor` from its element
 // 1024*row, whose state starts at element 1024*state_row.
 struct ChunkRec {
   uint32_t tensor;
