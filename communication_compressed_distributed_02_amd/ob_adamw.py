@@ -256,8 +256,11 @@ class _Plan(OnStream):
     def grad_norm(self, grads, grad_scale=1.0):
         """(norm as a float32 scalar, sum of squares as a float64 scalar) of
         the gradients (None: no gradient), on the device."""
-        b = grads if isinstance(grads, TensorBatch) else TensorBatch(
-            self, tuple(grads), self._ptrs(grads, self.grad_dtype, "gradients", True), (), None)
+        b = grads
+        if not isinstance(b, TensorBatch):
+            grads = tuple(grads)
+            b = TensorBatch(self, grads, self._ptrs(grads, self.grad_dtype, "gradients", True), (),
+                            None)
         if b.plan is not self:
             raise ValueError("a batch bound by another plan")
         norm, sumsq = torch.empty_like(self._like_norm), torch.empty_like(self._like_sumsq)
@@ -266,9 +269,11 @@ class _Plan(OnStream):
         return norm, sumsq
 
     def _wait(self, fn):
-        """fn(handle), a call that waits for the stream."""
+        """fn(handle), a call that waits for the plan's stream, and before it for
+        the caller's, where graphs of the plan's calls may have been replayed."""
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+        torch.cuda.current_stream(self.device).synchronize()
         with torch.cuda.device(self.device):
             return fn(self.h)
 
@@ -333,6 +338,7 @@ class AdamW(_Plan):
         if state_bits not in (8, 32):
             raise ValueError("state_bits is 8 or 32")
         self.param_dtype = dt
+        groups = None if groups is None else tuple(groups)
         self.n_groups = n_groups or (1 if groups is None else max(groups) + 1)
         cfg = make_config(len(params), self.n_groups, _TYPES[dt], _TYPES[gdt], state_bits, master,
                           stochastic, betas[0], betas[1], eps, seed)

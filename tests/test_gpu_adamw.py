@@ -594,6 +594,37 @@ def test_caller_and_library_on_different_streams(oa):
     torch.cuda.synchronize()
 
 
+def test_counts_and_copies_wait_for_replays_on_other_streams(oa):
+    """A graph replayed behind a few milliseconds of work on a stream other
+    than the plan's: the counts and a checkpoint hold its steps."""
+    import torch
+    side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    x, g = dev(np.ones(5000, F)), dev(np.ones(5000, F))
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    opt = oa.AdamW([x], groups=iter([0]), stream=side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        opt.step([g], 1e-3)
+    torch.cuda.synchronize()
+    assert float(opt.grad_norm(iter([g]))[1]) == 5000.0
+    for k in range(3):
+        with torch.cuda.stream(mine):
+            for _ in range(20):
+                big.add_(1.0)
+            graph.replay()
+            assert opt.steps == (k + 1, 0)
+    with torch.cuda.stream(mine):
+        for _ in range(20):
+            big.add_(1.0)
+        graph.replay()
+        saved = opt.checkpoint("cpu")
+    torch.cuda.synchronize()
+    again = oa.AdamW([x], stream=side, checkpoint=saved.cuda())
+    assert again.steps == opt.steps == (4, 0)
+    assert A.same(host(again.get("m", 0)), host(opt.get("m", 0)))
+
+
 def test_sum_over_ranks_replaces_the_own_sum(oa):
     """sumsq= clips by a sum that the caller formed, as ranks of a sharded
     model do after adding theirs."""
