@@ -177,6 +177,32 @@ def test_many_tensors_take_several_launches(oa):
         assert_state(opt, ref, "%d bits" % bits)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("chunks", [64, 65, 256, 257])
+def test_either_side_of_each_way_to_launch(oa, chunks, bits):
+    """Lists of as many chunks of 4096 elements as the ways to launch a step
+    end or begin at, with a tensor of no elements, one of one element and one
+    without a gradient among them; clipped, and skipped once."""
+    sizes = [0, 1, 5000, 4096 * (chunks - 3) - 255]  # 0, 1, 2 and chunks - 3 chunks
+    params, grads = make_inputs(sizes, chunks, 4)
+    xs = [dev(a, offset=i % 2) for i, a in enumerate(params)]
+    opt = oa.AdamW(xs, state_bits=bits, seed=9)
+    ref = A.Reference(params, opt.offsets, bits, seed=9)
+    for t, gs in enumerate(grads):
+        gs = list(gs)
+        if t == 1:
+            gs[2] = None
+        if t == 2:
+            gs[3][-1] = np.inf
+            opt.step([dev(g) for g in gs], 1e-3, 0.1, max_norm=0.5, skip_nonfinite=True)
+        else:
+            opt.step([None if g is None else dev(g) for g in gs], 1e-3, 0.1, max_norm=0.5,
+                     skip_nonfinite=True)
+            ref.step(gs, 1e-3, 0.1, 0.5)
+        assert_state(opt, ref, "step %d" % t)
+    assert opt.steps == (3, 1)
+
+
 def test_tensor_without_gradient_is_left_alone(oa):
     sizes = [700, 2000, 5]
     params, grads = make_inputs(sizes, 6, 2)
