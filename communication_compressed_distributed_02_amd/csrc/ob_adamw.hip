@@ -66,11 +66,16 @@ hipError_t capturing(hipStream_t stream, bool* out) {
 }
 
 hipError_t upload(ob_adamw_handle* h, const std::vector<aw::ChunkRec>& recs) {
-  hipError_t e = hipSuccess;
-  if (!recs.empty())
-    e = hipMemcpyAsync(h->base + h->at.recs, recs.data(), recs.size() * sizeof(aw::ChunkRec),
-                       hipMemcpyHostToDevice, h->stream);
-  const hipError_t w = hipStreamSynchronize(h->stream);  // recs goes with the caller
+  if (recs.empty()) return hipSuccess;
+  return hipMemcpyAsync(h->base + h->at.recs, recs.data(), recs.size() * sizeof(aw::ChunkRec),
+                        hipMemcpyHostToDevice, h->stream);
+}
+
+// Waits for what was enqueued, whether all of it was (e): the uploaded list goes
+// with the caller, who may write the parameters and the workspace on any stream
+// from then on.
+hipError_t settle(ob_adamw_handle* h, hipError_t e) {
+  const hipError_t w = hipStreamSynchronize(h->stream);
   return e != hipSuccess ? e : w;
 }
 
@@ -245,7 +250,7 @@ ob_status ob_adamw_init(const ob_adamw_config* cfg, const int64_t* numel, const 
         return aw::launch_master(h->st, p, (uint32_t)s.t0, c, n, h->stream);
       });
     }
-    return e == hipSuccess ? OB_OK : OB_ERR_HIP;
+    return settle(h, e) == hipSuccess ? OB_OK : OB_ERR_HIP;
   });
   if (st != OB_OK) {
     delete h;
@@ -263,7 +268,7 @@ ob_status ob_adamw_attach(const ob_adamw_config* cfg, const int64_t* numel, cons
     std::vector<aw::ChunkRec> recs;
     const ob_status r = make(cfg, numel, group, workspace, ws_bytes, stream, &recs, &h);
     if (r != OB_OK) return r;
-    return upload(h, recs) == hipSuccess ? OB_OK : OB_ERR_HIP;
+    return settle(h, upload(h, recs)) == hipSuccess ? OB_OK : OB_ERR_HIP;
   });
   if (st != OB_OK) {
     delete h;

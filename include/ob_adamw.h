@@ -102,8 +102,10 @@ ob_status ob_adamw_layout(const ob_adamw_config* cfg, const int64_t* numel, int6
 /* A plan over `workspace` with zero moments and step count 0.  group: host
  * array, tensor i's hyperparameter group (NULL: all 0).  params: host array
  * of device pointers as for ob_adamw_step, read for the master copies; NULL =
- * zeros, and ignored without `master`.  Waits for the stream (its tables are
- * uploaded from the call's own memory); OB_ERR_PHASE on a capturing stream. */
+ * zeros, and ignored without `master`.  Waits for the stream: when it returns,
+ * the plan's tables are uploaded, the parameters have been read and the whole
+ * workspace is written, so either may be written on any stream; OB_ERR_PHASE
+ * on a capturing stream. */
 ob_status ob_adamw_init(const ob_adamw_config* cfg, const int64_t* numel, const int32_t* group,
                         void* workspace, uint64_t ws_bytes, const void* const* params,
                         void* stream, ob_adamw_t* out);
@@ -111,7 +113,8 @@ ob_status ob_adamw_init(const ob_adamw_config* cfg, const int64_t* numel, const 
 /* Like ob_adamw_init, but adopts the state of a copy of a workspace of the
  * same configuration and sizes: the workspace bytes are the whole state, the
  * step count among them, and later steps are bit-identical to those of an
- * uninterrupted run.  (The plan's own tables are written again.) */
+ * uninterrupted run.  (The plan's own tables are written again, and the stream
+ * is waited for.) */
 ob_status ob_adamw_attach(const ob_adamw_config* cfg, const int64_t* numel, const int32_t* group,
                           void* workspace, uint64_t ws_bytes, void* stream, ob_adamw_t* out);
 
