@@ -198,23 +198,31 @@ class _Plan(OnStream):
         with torch.cuda.device(self.device):
             self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
             self._stream_ptr = self.stream.cuda_stream
-            if checkpoint is not None and checkpoint.numel() != self.ws_bytes:
-                raise ValueError("checkpoint of %d bytes, workspace needs %d"
-                                 % (checkpoint.numel(), self.ws_bytes))
+            if checkpoint is not None:
+                self._check_size(checkpoint)
             # what results are made like: a third less time than naming a type and device
             self._like_norm = torch.empty((), dtype=torch.float32, device=self.device)
             self._like_sumsq = torch.empty((), dtype=torch.float64, device=self.device)
             self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
             self._order_after_caller(self.workspace)
             if checkpoint is not None:
-                with torch.cuda.stream(self.stream):
-                    self.workspace.copy_(checkpoint)
-                self.h = ob_adamw_attach(cfg, self.numels, self.groups,
-                                         self.workspace.data_ptr(), self.ws_bytes,
-                                         self.stream.cuda_stream)
+                self.h = self._adopt(checkpoint)
             else:
                 self.h = ob_adamw_init(cfg, self.numels, self.groups, self.workspace.data_ptr(),
                                        self.ws_bytes, params, self.stream.cuda_stream)
+
+    def _check_size(self, checkpoint):
+        if checkpoint.numel() != self.ws_bytes:
+            raise ValueError("checkpoint of %d bytes, workspace needs %d"
+                             % (checkpoint.numel(), self.ws_bytes))
+
+    def _adopt(self, checkpoint):
+        """A handle over the workspace with the checkpoint's bytes in it, made on
+        the plan's stream, which is waited for."""
+        with torch.cuda.stream(self.stream):
+            self.workspace.copy_(checkpoint)
+        return ob_adamw_attach(self.cfg, self.numels, self.groups, self.workspace.data_ptr(),
+                               self.ws_bytes, self.stream.cuda_stream)
 
     def _call(self, lists, fn, *args):
         """fn(*args) with this plan's device current, ordered with the
@@ -466,6 +474,20 @@ class AdamW(_Plan):
     def steps(self):
         """(steps taken, steps skipped), replays among them (synchronizes)."""
         return self._wait(ob_adamw_get_steps)
+
+    def load(self, checkpoint):
+        """Go on from the workspace bytes of checkpoint() of a plan with the
+        same configuration and sizes.  They are copied to where the workspace
+        lies, so graphs captured from this plan go on from them too.
+        (Synchronizes.)"""
+        self._check_size(checkpoint)
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+        with torch.cuda.device(self.device):
+            self._order_after_caller()
+            h = self._adopt(checkpoint)
+        self.close()
+        self.h = h
 
     def checkpoint(self, device="cpu"):
         """A copy of the workspace bytes: the whole optimizer state."""

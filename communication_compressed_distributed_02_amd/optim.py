@@ -169,11 +169,9 @@ class AdamWOptimizer(torch.optim.Optimizer):
         self.params = [p for g in self.param_groups for p in g["params"]]
         groups = [i for i, g in enumerate(self.param_groups) for _ in g["params"]]
         self.max_norm, self.skip_nonfinite, self.norm = max_norm, skip_nonfinite, None
-        self._make = lambda checkpoint=None: oa.AdamW(
-            [p.detach() for p in self.params], groups, len(self.param_groups), grad_dtype,
-            state_bits, master, stochastic, betas, eps, seed, stream=stream,
-            checkpoint=checkpoint)
-        self._core = self._make()
+        self._core = oa.AdamW([p.detach() for p in self.params], groups, len(self.param_groups),
+                              grad_dtype, state_bits, master, stochastic, betas, eps, seed,
+                              stream=stream)
 
     @property
     def core(self):
@@ -235,10 +233,11 @@ class AdamWOptimizer(torch.optim.Optimizer):
 
     def load_state_dict(self, state):
         """A state_dict() of an optimizer made with the same arguments over
-        parameters of the same sizes."""
+        parameters of the same sizes.  The state is loaded where it lies, so steps
+        captured before go on from it."""
         if (state["numels"] != list(self._core.numels)
                 or len(state["param_groups"]) != len(self.param_groups)):
             raise ValueError("state of other parameters")
-        self._core = self._make(state["workspace"])
+        self._core.load(state["workspace"])
         for g, saved in zip(self.param_groups, state["param_groups"]):
             g.update(saved)
