@@ -199,7 +199,7 @@ class _Plan(OnStream):
             self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
             self._stream_ptr = self.stream.cuda_stream
             if checkpoint is not None:
-                self._check_size(checkpoint)
+                self._check_bytes(checkpoint)
             # what results are made like: a third less time than naming a type and device
             self._like_norm = torch.empty((), dtype=torch.float32, device=self.device)
             self._like_sumsq = torch.empty((), dtype=torch.float64, device=self.device)
@@ -211,7 +211,9 @@ class _Plan(OnStream):
                 self.h = ob_adamw_init(cfg, self.numels, self.groups, self.workspace.data_ptr(),
                                        self.ws_bytes, params, self.stream.cuda_stream)
 
-    def _check_size(self, checkpoint):
+    def _check_bytes(self, checkpoint):
+        if checkpoint.dtype != torch.uint8:
+            raise ValueError("a checkpoint is a uint8 tensor, not " + str(checkpoint.dtype))
         if checkpoint.numel() != self.ws_bytes:
             raise ValueError("checkpoint of %d bytes, workspace needs %d"
                              % (checkpoint.numel(), self.ws_bytes))
@@ -480,7 +482,7 @@ class AdamW(_Plan):
         same configuration and sizes.  They are copied to where the workspace
         lies, so graphs captured from this plan go on from them too.
         (Synchronizes.)"""
-        self._check_size(checkpoint)
+        self._check_bytes(checkpoint)
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("this call waits for the GPU: not while a graph is captured")
         with torch.cuda.device(self.device):

@@ -159,7 +159,8 @@ class AdamWOptimizer(torch.optim.Optimizer):
     by the global gradient norm (0: no clipping), without a host wait; the last
     norm is in `norm` on the device.  skip_nonfinite: a step whose gradients are
     not all finite changes nothing.  A parameter without a gradient is left as it
-    is.  state_dict() / load_state_dict() carry the library's whole state."""
+    is.  state_dict() / load_state_dict() carry the library's whole state and what it
+    was made with, all of which but grad_dtype has to be the same where it is loaded."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                  state_bits=32, master=False, stochastic=False, grad_dtype=None, max_norm=0.0,
@@ -225,9 +226,20 @@ class AdamWOptimizer(torch.optim.Optimizer):
         """(steps taken, steps skipped); waits for the GPU."""
         return self._core.steps
 
+    def _config(self):
+        """What the state depends on, in plain types: the powers of the betas are
+        part of it, and the rest decides what its bytes mean and how it goes on."""
+        core = self._core
+        return {"state_bits": core.cfg.state_bits, "param_dtype": str(core.param_dtype),
+                "master": bool(core.cfg.master), "stochastic": bool(core.cfg.stochastic),
+                "betas": [core.cfg.beta1, core.cfg.beta2], "eps": core.cfg.eps,
+                "seed": core.cfg.seed, "groups": list(core.groups)}
+
     def state_dict(self):
-        """The library's state (workspace bytes on the CPU) and the groups' rates."""
+        """The library's state (workspace bytes on the CPU), what it was made with
+        and the groups' rates."""
         return {"workspace": self._core.checkpoint("cpu"), "numels": list(self._core.numels),
+                "config": self._config(),
                 "param_groups": [{k: v for k, v in g.items() if k != "params"}
                                  for g in self.param_groups]}
 
@@ -238,6 +250,12 @@ class AdamWOptimizer(torch.optim.Optimizer):
         if (state["numels"] != list(self._core.numels)
                 or len(state["param_groups"]) != len(self.param_groups)):
             raise ValueError("state of other parameters")
+        # a state saved before it had one is taken by its sizes
+        for name, own in self._config().items():
+            saved = state.get("config", {}).get(name, own)
+            if saved != own:
+                raise ValueError("state of an optimizer with %s %r, this one has %r"
+                                 % (name, saved, own))
         self._core.load(state["workspace"])
         for g, saved in zip(self.param_groups, state["param_groups"]):
             g.update(saved)
