@@ -492,6 +492,16 @@ class AdamW(_Plan):
         self.h = h
 
     def checkpoint(self, device="cpu"):
-        """A copy of the workspace bytes: the whole optimizer state."""
-        self.stream.synchronize()
-        return self.workspace.to(device, copy=True)
+        """A copy of the workspace bytes: the whole optimizer state.  Taken on
+        the plan's stream, between what the caller's holds so far and the calls
+        that follow, from whichever stream they come."""
+        with torch.cuda.device(self.device):
+            self._order_after_caller()
+            with torch.cuda.stream(self.stream):
+                copy = self.workspace.to(device, copy=True)
+            if self._separate():
+                current = torch.cuda.current_stream(self.device)
+                current.wait_stream(self.stream)
+                if copy.device == self.device:
+                    copy.record_stream(current)
+        return copy

@@ -169,3 +169,28 @@ def test_states_of_other_optimizers_are_refused(oa):
     other.step()
     other.load_state_dict(old)
     assert other.steps == (2, 0)
+
+
+def test_checkpoint_is_taken_before_later_calls_from_other_streams(oa):
+    """A device copy asked for behind a few milliseconds of work on one stream,
+    then a step from another: the copy is of the state before that step."""
+    import torch
+    side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+    x, g = dev(np.ones(5000, F)), dev(np.ones(5000, F))
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    opt = oa.AdamW([x], stream=side)
+    for k in range(3):
+        opt.step([g], 1e-3)
+        before = host(opt.get("m", 0))
+        with torch.cuda.stream(mine):
+            for _ in range(20):
+                big.add_(1.0)
+            saved = opt.checkpoint("cuda")
+        opt.step([g], 1e-3)
+        after = host(opt.get("m", 0))
+        with torch.cuda.stream(mine):
+            saved = saved.cpu()
+        again = oa.AdamW([x], stream=side, checkpoint=saved)
+        assert again.steps == (2 * k + 1, 0) and opt.steps == (2 * k + 2, 0)
+        assert A.same(host(again.get("m", 0)), before) and not A.same(after, before)
