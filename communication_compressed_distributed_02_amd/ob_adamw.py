@@ -194,6 +194,7 @@ class _Plan(OnStream):
             raise ValueError("tensors on %s: a GPU is needed" % self.device)
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._not_capturing()
         self.offsets, self.length, self.ws_bytes = ob_adamw_layout(cfg, self.numels)
         with torch.cuda.device(self.device):
             self.stream = stream if stream is not None else torch.cuda.current_stream(self.device)
@@ -278,11 +279,17 @@ class _Plan(OnStream):
                    sumsq.data_ptr(), norm.data_ptr())
         return norm, sumsq
 
+    @staticmethod
+    def _not_capturing():
+        """Raises where the current stream is under capture, before anything is
+        enqueued there or waited for, so that the capture goes on."""
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+
     def _wait(self, fn):
         """fn(handle), a call that waits for the plan's stream, and before it for
         the caller's, where graphs of the plan's calls may have been replayed."""
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+        self._not_capturing()
         torch.cuda.current_stream(self.device).synchronize()
         with torch.cuda.device(self.device):
             return fn(self.h)
@@ -483,8 +490,7 @@ class AdamW(_Plan):
         lies, so graphs captured from this plan go on from them too.
         (Synchronizes.)"""
         self._check_bytes(checkpoint)
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("this call waits for the GPU: not while a graph is captured")
+        self._not_capturing()
         with torch.cuda.device(self.device):
             self._order_after_caller()
             h = self._adopt(checkpoint)
@@ -495,6 +501,7 @@ class AdamW(_Plan):
         """A copy of the workspace bytes: the whole optimizer state.  Taken on
         the plan's stream, between what the caller's holds so far and the calls
         that follow, from whichever stream they come."""
+        self._not_capturing()
         with torch.cuda.device(self.device):
             self._order_after_caller()
             with torch.cuda.stream(self.stream):

@@ -194,3 +194,33 @@ def test_checkpoint_is_taken_before_later_calls_from_other_streams(oa):
         again = oa.AdamW([x], stream=side, checkpoint=saved)
         assert again.steps == (2 * k + 1, 0) and opt.steps == (2 * k + 2, 0)
         assert A.same(host(again.get("m", 0)), before) and not A.same(after, before)
+
+
+def test_calls_that_wait_are_refused_under_capture(oa):
+    """Plans made, loaded, copied and asked for their counts while the current
+    stream is captured, with the plan on that stream or on one of its own: each
+    is refused, and the capture goes on with what it had."""
+    import torch
+    for own in (False, True):
+        side, mine = torch.cuda.Stream(), torch.cuda.Stream()
+        stream = side if own else mine
+        x, g, y = (dev(np.ones(5000, F)) for _ in range(3))
+        torch.cuda.synchronize()
+        opt = oa.AdamW([x], stream=stream)
+        saved = opt.checkpoint()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=mine):
+            y.add_(1.0)
+            for call in (opt.checkpoint, lambda: opt.checkpoint("cuda"), lambda: opt.load(saved),
+                         lambda: opt.steps, opt.check_guards,
+                         lambda: oa.AdamW([x], stream=stream), lambda: oa.GradNorm([x]),
+                         lambda: oa.AdamW([x], stream=stream, checkpoint=saved)):
+                with pytest.raises(RuntimeError):
+                    call()
+            opt.step([g], 1e-3)
+        torch.cuda.synchronize()
+        for k in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert float(y[0]) == 2.0 + k and opt.steps == (k + 1, 0)
