@@ -65,3 +65,34 @@ def test_init_has_read_the_parameters_when_it_returns(shim, oa, sizes):
     with Handle(shim, oa, sizes, True, param_dtype=oa.OB_ADAMW_BF16, master=True) as h:
         assert "m" in h.made and "u" in h.made and h.made.endswith("w")
         assert max(h.made.rfind(c) for c in "mfut") < h.made.index("w")
+
+
+def power(beta, steps):
+    """beta^steps by as many products in double precision, stopping where a
+    product changes nothing."""
+    p = 1.0
+    for _ in range(steps):
+        q = p * beta
+        if q == p:
+            break
+        p = q
+    return p
+
+
+def test_steps_are_set_without_walking_over_powers_that_no_longer_change(shim, oa):
+    """A power of a beta above a half ends among the smallest denormals, not at
+    zero.  The slowest beta here is there after some 750 000 products, a few
+    milliseconds; the 2^31 - 1 that are allowed take seconds to minutes."""
+    import time
+    f32 = [ctypes.c_float(b).value for b in (0.0, 0.25, 0.5, 0.6, 0.9, 0.98, 0.999)]
+    last = (1 << 31) - 1
+    for b1, b2 in zip(f32, f32[1:] + f32[:1]):
+        with Handle(shim, oa, [100], beta1=b1, beta2=b2) as h:
+            got = (ctypes.c_double * 2)()
+            for steps in (0, 1, 7, 7000, 800000, last):
+                t = time.monotonic()
+                assert shim.ob_adamw_set_steps(h.h, ctypes.c_int64(steps)) == 0
+                assert time.monotonic() - t < 0.5
+                shim.shim_powers(got)
+                assert tuple(got) == (power(b1, steps), power(b2, steps)), (b1, b2, steps)
+            assert 0.0 < power(0.9, last) < 1e-322
