@@ -410,7 +410,8 @@ __device__ __forceinline__ void step_groups(const GT* g, PT* p, const State& s, 
   const float b1 = s.beta1, ob1 = 1.0f - b1, b2 = s.beta2, ob2 = 1.0f - b2;
   const uint64_t quad0 = (uint64_t)group * (kScaleElems / 4);
   const uint32_t key0 = high_key(quad0, c.key0), key1 = c.key1;
-  const bool plain_scalars = s.eps >= 0x1p-30f && b2 >= 0x1p-10f;
+  const bool plain_scalars =
+      s.eps >= 0x1p-30f && b2 >= 0x1p-10f && (b1 == 0.0f || b1 >= 0x1p-8f);
   uint32_t new_me = 0, new_ve = 0;
 #pragma unroll
   for (int u = 0; u < GROUPS; ++u) {
@@ -442,9 +443,10 @@ __device__ __forceinline__ void step_groups(const GT* g, PT* p, const State& s, 
       st_stream((f32x4*)(v32 + o), v);
     } else {
       const uint32_t em = (me >> (8 * u)) & 255u, ev = (ve >> (8 * u)) & 255u;
-      // No code of v is special and m's scale times b1 is a normal number:
-      // then v stays above zero and decoding needs no exceptions.  (A v that
-      // is not finite comes from such a gradient, and so with such an m.)
+      // No code of v is special and m's scale (at least 2^-118) times b1 is a
+      // normal number or 0: then v stays above zero and decoding needs no
+      // exceptions.  (A v that is not finite comes from such a gradient, and so
+      // with such an m.)
       bool plain = plain_scalars && em >= 16u && __ballot(special_codes(vc[u])) == 0;
       if (plain) {
         // b1 * (code * 2^k) rounds as (b1 * 2^k) * code does
