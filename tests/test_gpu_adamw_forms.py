@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import adamw_common as A
+import test_gpu_adamw as T
 from test_gpu_adamw import dev, host
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +86,66 @@ def test_updates_under_a_large_eps(oa, eps):
     bad = np.abs(x.astype(np.float64) - want) > 15 * U * np.abs(want)
     assert not bad.any(), (eps, x[bad][:3], want[bad][:3])
     assert np.array_equal(codes, c) and np.array_equal(exps, e)
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("bits,stochastic", [(32, False), (32, True), (8, False)])
+def test_bfloat16_parameters_without_copies_under_float32_gradients(oa, bits, stochastic, many):
+    """Ragged, unaligned, in one launch and in several, as the other kinds."""
+    T.test_steps_equal_the_plain_form(oa, "bf16", "f32", bits, False, stochastic, many)
+
+
+@pytest.mark.parametrize("g,big", [("f32", 17090 * 4096 + 1234), ("bf16", 32001 * 4096 + 77)])
+def test_lists_past_every_round_and_launch(oa, g, big):
+    """Lists so long that a block of the norm takes several chunks, not equally
+    many (more than 2048 of them in a launch), the fold a second round (more
+    than 2048 partial sums), the norm in front of a step leaves the first 240
+    MB in the caches and streams the rest (15360 chunks of float32 gradients,
+    30720 of bfloat16), and a step two launches (more than 2^14 chunks) beside
+    those of its tensors.  The gradients are small whole numbers, so S is exact
+    in 64 bits whatever the order, and a chunk left out or taken twice shows;
+    every element of m and v is compared, and the parameters around the places
+    where launches and rounds meet."""
+    import math
+
+    import torch
+    sizes = [1 + 61 * i % 9001 for i in range(500)]
+    sizes[7], sizes[490] = big, 3 * 4096 + 1
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[g]
+    gen = torch.Generator(device="cuda").manual_seed(44)
+    gs = [torch.randint(-3, 4, (n,), device="cuda", generator=gen).to(dt) for n in sizes]
+    xs = [torch.randn(n, device="cuda", generator=gen).mul_(0.1) for n in sizes]
+    total = sum(int(a.to(torch.int32).square_().sum(dtype=torch.int64)) for a in gs)
+    assert total < 1 << 53
+    norm, s = oa.GradNorm(gs).grad_norm(gs)
+    assert float(s) == total and float(norm) == F(math.sqrt(total))
+    chunks = [-(-n // 4096) for n in sizes]
+    launch = sum(chunks[:240])  # the first 240 tensors' chunks, in equal launches
+    parts = -(-launch // (1 << 14))
+    assert parts > 1 and len(sizes) > 480 and launch % 2048
+    marks = [0, 2048, 4096, 15360, 30720] + [k * -(-launch // parts) for k in range(1, parts)]
+    spots = {big - 300}
+    for c in marks:
+        at = 4096 * (c - sum(chunks[:7]))  # where chunk c lies in the big tensor
+        spots.update(min(max(at + k * 4096 - 300, 0), big - 300) for k in (-1, 0, 1))
+    pieces = {a: host(xs[7][a:a + 600]) for a in sorted(spots)}
+    whole = {i: host(xs[i]) for i in (0, 3, 6, 8, 239, 240, 241, 479, 480, 490, 499)}
+    opt = oa.AdamW(xs, grad_dtype=dt)
+    got = opt.step(gs, 1e-2, 0.1, max_norm=1.0)
+    assert float(got) == F(math.sqrt(total))
+    gscale = float(F(1.0 / math.sqrt(total)))
+    ob1, ob2 = float(A.OB1), float(A.OB2)
+    view = opt.views()
+    for i, a in enumerate(gs):
+        at, n = opt.offsets[i], sizes[i]
+        scaled = a.float() * gscale
+        assert torch.equal(view["m"][at:at + n], scaled * ob1), i
+        assert torch.equal(view["v"][at:at + n], (scaled * scaled) * ob2), i
+        del scaled
+    rows = [(a, xs[7][a:a + 600], gs[7][a:a + 600], p) for a, p in pieces.items()]
+    rows += [(i, xs[i], gs[i], p) for i, p in whole.items()]
+    for where, x, a, p in rows:
+        zeros = np.zeros(p.size, F)
+        want = A.step32(p, zeros, zeros, host(a), 1, 1e-2, 0.1, gscale)[0]
+        assert A.same(host(x), want), where
+    assert opt.check_guards() == -1 and opt.steps == (1, 0)
