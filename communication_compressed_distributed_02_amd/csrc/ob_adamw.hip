@@ -149,17 +149,17 @@ hipError_t launches(ob_adamw_t h, const aw::Span& s, F fn) {
   return e;
 }
 
-// The partial sums of squares of every span; in front of a step (keep) the
-// first span last, with which the step begins.
-hipError_t norm_pass(ob_adamw_t h, const void* const* grads, bool keep) {
+// The partial sums of squares of every span; in front of a step (backwards)
+// the first span last, with which the step begins.
+hipError_t norm_pass(ob_adamw_t h, const void* const* grads, bool backwards) {
   const size_t spans = h->plan.norm_spans.size();
   int64_t at = 0;
   for (size_t i = 0; i < spans; ++i) {
-    const aw::Span& s = h->plan.norm_spans[keep ? spans - 1 - i : i];
+    const aw::Span& s = h->plan.norm_spans[backwards ? spans - 1 - i : i];
     aw::NormPtrs p;
     for (int32_t k = 0; k < s.n; ++k) p.g[k] = grads[s.t0 + k];
     const hipError_t e =
-        aw::launch_norm(h->st, p, (uint32_t)s.t0, s.c0, s.chunks, at, keep, h->stream);
+        aw::launch_norm(h->st, p, (uint32_t)s.t0, s.c0, s.chunks, at, backwards, h->stream);
     if (e != hipSuccess) return e;
     at += aw::norm_partials(s.chunks);
   }

@@ -85,9 +85,10 @@ hipError_t launch_small_norm(const SmallNorm& k, bool grad_bf16, int64_t n, hipS
 hipError_t launch_step(const State& s, const StepPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
                        hipStream_t stream);
 // The same for the norm, leaving norm_partials(n) values from partials[at].
-// keep: a step follows (its first gradients are left in the caches).
+// backwards: a step follows; the chunks go from the last to the first, through
+// the caches.
 hipError_t launch_norm(const State& s, const NormPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
-                       int64_t at, bool keep, hipStream_t stream);
+                       int64_t at, bool backwards, hipStream_t stream);
 // Folds the partials (or reads sumsq) and advances the step.
 hipError_t launch_control(const State& s, const ControlArgs& a, hipStream_t stream);
 // Folds the partials into the caller's sumsq and norm.

@@ -25,8 +25,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int64_t kKeptBytes = int64_t(240) << 20;  // gradients that a norm leaves in the caches
-
 constexpr int kGroups = kRowElems / kScaleElems;  // groups of 256 in a row of 1024
 
 struct bf16 {
@@ -63,8 +61,8 @@ __device__ __forceinline__ f32x4 load4(const float* p) {
 __device__ __forceinline__ u32x2 load_packed(const bf16* p) {
   return __builtin_nontemporal_load((const u32x2_at2*)p);
 }
-// The same, left in the caches.
-__device__ __forceinline__ f32x4 load4_kept(const float* p) { return *(const f32x4_at4*)p; }
+// The same through the caches.
+__device__ __forceinline__ f32x4 load4_cached(const float* p) { return *(const f32x4_at4*)p; }
 __device__ __forceinline__ f32x4 widen2(u32x2 w) {
   return f32x4{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
                __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)};
@@ -72,7 +70,7 @@ __device__ __forceinline__ f32x4 widen2(u32x2 w) {
 __device__ __forceinline__ f32x4 load4(const bf16* p) {
   return widen2(load_packed(p));
 }
-__device__ __forceinline__ f32x4 load4_kept(const bf16* p) {
+__device__ __forceinline__ f32x4 load4_cached(const bf16* p) {
   return widen2(*(const u32x2_at2*)p);
 }
 // The first n (0 to 4) of them at element alignment, zeros after.
@@ -603,21 +601,23 @@ __device__ __forceinline__ double row_sum(const GT* p, int left, int at) {
   return add_squares(0.0, v);
 }
 
-// In front of a step (kept > 0) a span's chunks go from the last to the first,
-// and the first `kept` chunks of the plan are loaded through the caches where
-// the rest streams past them: the step starts with those and finds their
-// gradients in the 256 MB memory-side cache (clipped step of 334M parameters,
-// bfloat16 gradients: 1544 us with none kept, 1525 with 128 MB, 1506 with 240
-// MB).  A norm on its own streams everything from the first chunk on, 1 %
+// In front of a step (BACKWARDS) a span's chunks go from the last to the first
+// and are loaded through the caches: the step starts on the gradients that were
+// read last and finds part of them in the 256 MB memory-side cache.  Clipped
+// steps with that, backwards past the caches, and forwards past them: 334M
+// parameters 1457, 1477 and 1478 us (32-bit states, bfloat16 gradients), 1085,
+// 1098 and 1100 (8-bit, fp32), 13M in 61 tensors 73.2, 74.8 and 75.0, 38.7, 38.8
+// and 39.6; 1.56B parameters 7.635, 7.641 and 7.643 ms, but with 8-bit states
+// 3.031, 3.012 and 3.016.  A norm on its own goes forwards past the caches, 1 %
 // faster than backwards (6.2 GB: 936 and 945 us).
-template <typename GT, bool KEEP>
+template <typename GT, bool BACKWARDS>
 __global__ void __launch_bounds__(kBlock)
     norm_kernel(NormPtrs ptrs, const ChunkRec* __restrict__ recs, uint32_t t0, int64_t c0,
-                int64_t n, int64_t kept, double* __restrict__ partials) {
+                int64_t n, double* __restrict__ partials) {
   __shared__ double red[kBlock / 64];
   const int wave = wave_in_block();
   const int at = (threadIdx.x & 63) * 4;
-  const auto chunk = [&](int64_t i) { return KEEP ? c0 + n - 1 - i : c0 + i; };
+  const auto chunk = [&](int64_t i) { return BACKWARDS ? c0 + n - 1 - i : c0 + i; };
   double acc = 0.0;
   int64_t i = blockIdx.x;
   ChunkRec rec = recs[chunk(i)];
@@ -627,12 +627,10 @@ __global__ void __launch_bounds__(kBlock)
     const GT* p = g + ((int64_t)rec.row + wave) * kRowElems + at;
     f32x4 v[kGroups];
     if (left >= kRowElems) {
-      if (KEEP && chunk(i) < kept) {
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) v[u] = load4_kept(p + u * kScaleElems);
-      } else {
-#pragma unroll
-        for (int u = 0; u < kGroups; ++u) v[u] = load4(p + u * kScaleElems);
+      for (int u = 0; u < kGroups; ++u) {
+        if constexpr (BACKWARDS) v[u] = load4_cached(p + u * kScaleElems);
+        else v[u] = load4(p + u * kScaleElems);
       }
     } else {
 #pragma unroll
@@ -1092,12 +1090,12 @@ hipError_t launch_small(const SmallStep& k, int64_t n, hipStream_t stream) {
 }
 
 hipError_t launch_norm(const State& s, const NormPtrs& ptrs, uint32_t t0, int64_t c0, int64_t n,
-                       int64_t at, bool keep, hipStream_t stream) {
+                       int64_t at, bool backwards, hipStream_t stream) {
   const unsigned grid = (unsigned)norm_partials(n);
-  const int64_t kept = kKeptBytes / (kChunkElems * (s.grad_bf16 ? 2 : 4));
-  const auto kernel = s.grad_bf16 ? (keep ? norm_kernel<bf16, true> : norm_kernel<bf16, false>)
-                                  : (keep ? norm_kernel<float, true> : norm_kernel<float, false>);
-  kernel<<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, kept, s.partials + at);
+  const auto kernel =
+      s.grad_bf16 ? (backwards ? norm_kernel<bf16, true> : norm_kernel<bf16, false>)
+                  : (backwards ? norm_kernel<float, true> : norm_kernel<float, false>);
+  kernel<<<grid, kBlock, 0, stream>>>(ptrs, s.recs, t0, c0, n, s.partials + at);
   return hipGetLastError();
 }
 
