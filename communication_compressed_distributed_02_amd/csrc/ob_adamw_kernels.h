@@ -28,7 +28,7 @@ struct Control {
   float gscale, rbc2;
   uint32_t skip, k0, k1;
   uint32_t root;             // tickets of small launches: leaves that are done
-  uint32_t leaf[kLeaves][16];  // and tickets taken, each counter in a line of its own
+  uint32_t leaf[kLeaves][16];  // and tickets taken, 64 bytes apart
   float decay[kMaxGroups], rate[kMaxGroups];
 };
 

@@ -5,9 +5,10 @@
 // groups of 256, of which a lane takes 4 consecutive elements.  A group is the
 // unit that shares the exponents of an 8-bit state, so its maximum is a
 // reduction over one wave's lanes, in registers.  A wave takes 4 groups of the
-// norm, and 1 or 2 of the step (kStepGroups).  The list of chunks (tensor,
-// place, length, hyperparameter group) is made once per plan; the tensors'
-// pointers come by value with each launch.
+// norm, 1 or 2 of a step over many chunks (kStepGroups) and 1 or 4 of a step
+// over few (kFewChunks).  The list of chunks (tensor, place, length,
+// hyperparameter group) is made once per plan; the tensors' pointers come by
+// value with each launch.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -1010,9 +1011,11 @@ int grid_for(int64_t threads) {
   return (int)(blocks < 1 ? 1 : (blocks > 8192 ? 8192 : blocks));
 }
 
-// A wave takes one group where a step has so few chunks, four else: the latency
-// of one wave's instructions shows.  8-bit states, 16 chunks 4.8 and 6.2 us, 64
-// chunks 6.0 and 6.3, 128 chunks 7.2 and 6.4 (four times the tickets).
+// A wave of a small step takes one group where there are so few chunks, four
+// else: the latency of one wave's instructions shows below, four times the
+// tickets above.  One and four groups, 32-bit states: 16 chunks 4.4 and 5.3 us,
+// 64 chunks 5.8 and 6.0, 128 chunks 7.4 and 6.5, 256 chunks 10.6 and 7.3; 8-bit
+// ones: 4.4 and 5.8, 5.7 and 5.9, 7.0 and 6.4, 10.2 and 7.4.
 constexpr int64_t kFewChunks = 64;
 
 // fn(types and kinds of the plan's step as compile-time values).

@@ -27,9 +27,13 @@ constexpr int kPtrsPerNorm = 480;
 constexpr int kNormBlocks = 2048;   // partial sums of one launch of the norm, at most
 // A step over at most so many chunks (2^20 elements) and tensors is one launch
 // without a control kernel in front, and a norm over them one without a
-// kernel behind.  32-bit states: 4.8 and 7.0 us at 8 chunks, 7.4 and 8.6 at
-// 256, 20.8 and 22.2 at 1024; 8-bit ones, clipped: 11.0 and 12.9 at 256, 14.6
-// and 13.4 at 512.
+// kernel behind (a partial sum a thread of the block that folds them).  The
+// step in one launch and in two, 32-bit states: 4.2 and 6.0 us at 4 chunks, 7.4
+// and 8.5 at 256, 10.5 and 13.3 at 512, 21.9 and 22.8 at 1024; 8-bit ones: 4.3
+// and 6.1 at 4, 7.5 and 7.2 at 256, 9.3 and 9.2 at 512, 15.2 and 14.6 at 1024.
+// Clipped, 32-bit: 11.3 and 13.0 at 256, 15.6 and 16.9 at 512, 30.5 and 27.0 at
+// 1024; 8-bit: 11.4 and 12.5, 14.6 and 13.3, 24.1 and 20.0.  So 256 is the limit
+// for 8-bit states; with 32-bit ones one launch would win at 512 as well.
 constexpr int kSmallChunks = 256;
 constexpr int kSmallTensors = 96;
 constexpr int kLeaves = 16;  // counters that the tickets of a small launch go over

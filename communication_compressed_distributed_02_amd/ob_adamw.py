@@ -336,9 +336,12 @@ class AdamW(_Plan):
     on one device), which the steps update where they lie.
 
     groups: each tensor's hyperparameter group (default all 0) of `n_groups`
-    (default: as many as are named).  grad_dtype: the gradients' type (default the parameters').  state_bits: 32 or 8.
-    master: keep float32 copies of bfloat16 parameters.  stochastic: round
-    bfloat16 parameters without copies stochastically.  seed: of the random
+    (default: as many as are named; at most OB_ADAMW_MAX_GROUPS).  grad_dtype:
+    the gradients' type (default the parameters').  state_bits: 32 or 8.
+    master: keep float32 copies of bfloat16 parameters, taken now: the steps go
+    on from the copies (`views()`, `set`), not from parameters that are written
+    between them.  stochastic: round bfloat16 parameters without copies
+    stochastically.  seed: of the random
     bits.  steps: steps already taken.  checkpoint: the workspace bytes of
     checkpoint() of a plan with the same configuration and sizes."""
 

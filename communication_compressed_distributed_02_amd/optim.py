@@ -153,9 +153,11 @@ class AdamWOptimizer(torch.optim.Optimizer):
     bfloat16 tensors of one type on one GPU, their .grad of `grad_dtype`
     (default the same type).
 
-    Groups may differ in lr and weight_decay, which are read from param_groups
-    at every step, so torch's LR schedulers drive it; betas and eps are common.
-    state_bits, master, stochastic and seed as for ob_adamw.AdamW.  max_norm: clip
+    Groups (at most 32) may differ in lr and weight_decay, which are read from
+    param_groups at every step, so torch's LR schedulers drive it; betas and eps
+    are common.  state_bits, master, stochastic and seed as for ob_adamw.AdamW:
+    with master, weights loaded into the model later are overwritten by the
+    copies at the next step.  max_norm: clip
     by the global gradient norm (0: no clipping), without a host wait; the last
     norm is in `norm` on the device.  skip_nonfinite: a step whose gradients are
     not all finite changes nothing.  A parameter without a gradient is left as it

@@ -39,9 +39,12 @@
  *    Rounding v to nearest would freeze it: a step moves v by about 1 - b2 of
  *    itself, the codes are 6 to 12 % apart.
  *    Beside 8-bit states the square root and the quotient are formed from
- *    one-ulp approximations (for 2^-30 <= eps), so that m / (...) is within
- *    7 * 2^-24 of its exact value, relatively; everything else rounds as
- *    stated.
+ *    one-ulp approximations, so that m / (...) is within 7 * 2^-24 of its exact
+ *    value, relatively; everything else rounds as stated.  They are rounded
+ *    correctly there too for eps < 2^-30, for beta2 < 2^-10, for 0 < beta1 <
+ *    2^-8, among a tensor's last 1023 elements where they do not fill a wave's
+ *    share, and in blocks of 256 that held a v of 0 or hold a moment that is
+ *    not finite or near the ends of fp32's range.
  *  - random bits: 32-bit words hashed from k/4 (k = the element's index in
  *    the state), the seed and the step count; elements 4i .. 4i+3 take the
  *    low and the high half of word 0, then of word 1, for v, and of words 2
@@ -80,7 +83,7 @@ enum { OB_ADAMW_MAX_GROUPS = 32 };
 
 typedef struct {
   int32_t n_tensors;   /* 1 .. 2^20 */
-  int32_t n_groups;    /* hyperparameter groups, 1 .. OB_ADAMW_MAX_GROUPS */
+  int32_t n_groups;    /* hyperparameter groups, 1 .. OB_ADAMW_MAX_GROUPS (OB_ERR_ARG) */
   int32_t param_dtype; /* OB_ADAMW_F32 or OB_ADAMW_BF16 */
   int32_t grad_dtype;  /* OB_ADAMW_F32 or OB_ADAMW_BF16 */
   int32_t state_bits;  /* 32, 8, or 0: a plan for gradient norms only */
