@@ -86,31 +86,43 @@ def _i64s(values):
     return (ctypes.c_int64 * max(1, len(values)))(*values)
 
 
+def _numels(cfg, numels):
+    if len(numels) != cfg.n_tensors:
+        raise ValueError("%d element counts given for %d tensors" % (len(numels), cfg.n_tensors))
+    return _i64s(numels)
+
+
 def ob_adamw_layout(cfg, numels):
     """(first state element of every tensor, elements of a state array,
     workspace bytes)."""
     offsets = _i64s([0] * len(numels))
     length, total = ctypes.c_int64(0), ctypes.c_uint64(0)
-    _check(_lib.ob_adamw_layout(ctypes.byref(cfg), _i64s(numels), offsets, ctypes.byref(length),
-                                ctypes.byref(total)), "ob_adamw_layout")
+    _check(_lib.ob_adamw_layout(ctypes.byref(cfg), _numels(cfg, numels), offsets,
+                                ctypes.byref(length), ctypes.byref(total)), "ob_adamw_layout")
     return list(offsets)[:len(numels)], length.value, total.value
 
 
-def _groups(groups):
-    return None if groups is None else (ctypes.c_int32 * len(groups))(*groups)
+def _groups(cfg, groups):
+    if groups is None:
+        return None
+    if len(groups) != cfg.n_tensors:
+        raise ValueError("%d groups given for %d tensors" % (len(groups), cfg.n_tensors))
+    return (ctypes.c_int32 * len(groups))(*groups)
 
 
 def ob_adamw_init(cfg, numels, groups, workspace_ptr, ws_bytes, param_ptrs, stream_ptr):
     h = ctypes.c_void_p(0)
-    _check(_lib.ob_adamw_init(ctypes.byref(cfg), _i64s(numels), _groups(groups), workspace_ptr,
-                              ws_bytes, param_ptrs, stream_ptr, ctypes.byref(h)), "ob_adamw_init")
+    _check(_lib.ob_adamw_init(ctypes.byref(cfg), _numels(cfg, numels), _groups(cfg, groups),
+                              workspace_ptr, ws_bytes, param_ptrs, stream_ptr, ctypes.byref(h)),
+           "ob_adamw_init")
     return h.value
 
 
 def ob_adamw_attach(cfg, numels, groups, workspace_ptr, ws_bytes, stream_ptr):
     h = ctypes.c_void_p(0)
-    _check(_lib.ob_adamw_attach(ctypes.byref(cfg), _i64s(numels), _groups(groups), workspace_ptr,
-                                ws_bytes, stream_ptr, ctypes.byref(h)), "ob_adamw_attach")
+    _check(_lib.ob_adamw_attach(ctypes.byref(cfg), _numels(cfg, numels), _groups(cfg, groups),
+                                workspace_ptr, ws_bytes, stream_ptr, ctypes.byref(h)),
+           "ob_adamw_attach")
     return h.value
 
 
@@ -185,9 +197,7 @@ class _Plan(OnStream):
                  params=None):
         self.cfg, self.numels, self.grad_dtype = cfg, list(numels), grad_dtype
         self.groups = None if groups is None else [int(g) for g in groups]
-        if self.groups is not None and len(self.groups) != len(self.numels):
-            raise ValueError("%d groups given for %d tensors" % (len(self.groups),
-                                                                 len(self.numels)))
+        _groups(cfg, self.groups)
         self.h = None
         self.device = torch.device(device)
         if self.device.type != "cuda":

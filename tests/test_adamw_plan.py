@@ -308,3 +308,18 @@ def test_fp32_form_is_within_its_bounds():
         x32, m32, v32 = A.step32(x, m, v, g, t, 1e-3, 0.01)
         for a, b, d in ((x32, x64, dx), (m32, m64, dm), (v32, v64, dv)):
             assert np.all(np.abs(a - b) <= d)
+
+
+def test_lists_of_other_lengths_than_the_configuration_are_refused(oa):
+    """The binding's functions read as many counts and groups as the
+    configuration names tensors."""
+    cfg = oa.make_config(3, 2)
+    for numels in ([], [5, 5], [5] * 4):
+        with pytest.raises(ValueError):
+            oa.ob_adamw_layout(cfg, numels)
+    for numels, groups in (([5, 5], None), ([5] * 3, [0, 1]), ([5] * 3, [0] * 4)):
+        with pytest.raises(ValueError):
+            oa.ob_adamw_init(cfg, numels, groups, None, 0, None, None)
+        with pytest.raises(ValueError):
+            oa.ob_adamw_attach(cfg, numels, groups, None, 0, None)
+    assert oa.ob_adamw_layout(cfg, [5] * 3)[1] == 3 * 1024
