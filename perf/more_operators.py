@@ -6,8 +6,9 @@ and a linear layer's forward and backward pass made of them.
 with the framework's kernels.  A quantised matrix holds blocks of 32
 consecutive elements of a row: 4-bit codes (sign, 2 exponent bits, 1 mantissa
 bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6) and one byte E, which scales them by
-2^(E - 127).  Rows are padded with zeros to a multiple of 128 elements;
-element 2i of a row is the low half of byte i.
+2^(E - 127).  Rows are padded with zeros, the codes to a multiple of 128
+elements, the scales to one of 16 bytes; element 2i of a row is the low half
+of byte i.
 
   c = fp32(x + e), or x widened where there is no residual e
   a = the block's largest |c|; E - 127 = the least k >= -127 with a < 7 * 2^k
@@ -29,7 +30,8 @@ import torch
 own = False
 
 BLOCK = 32   # elements of one scale
-PAD = 128    # rows end at a multiple of this
+PAD = 128    # rows of codes end at a multiple of this
+SCALES = 16  # rows of scales end at a multiple of this
 MASK = 0xFFFFFFFF
 # odd multipliers of the hash: digits of the square roots of 2, 3 and 5 and of the golden ratio
 ROOT2, ROOT3, ROOT5 = 0x6A09E667F3BCC909, 0xBB67AE8584CAA73B, 0x3C6EF372FE94F82B
@@ -111,7 +113,11 @@ def padded(cols):
 
 
 def packed_bytes(rows, cols):
-    return rows * padded(cols) * 17 // 32
+    return rows * (padded(cols) // 2 + scale_bytes(cols))
+
+
+def scale_bytes(cols):
+    return -(-cols // (BLOCK * SCALES)) * SCALES
 
 
 def work(case):
@@ -263,17 +269,18 @@ def pack(c):
     code = torch.where(mag < 2, mag * 2, torch.where(mag < 4, mag + 2, mag * 0.5 + 4))
     code = code.to(torch.uint8) | (torch.signbit(v).to(torch.uint8) << 3)
     code = code.view(c.shape[0], -1, 2)
-    return {"codes": code[:, :, 0] | (code[:, :, 1] << 4), "scales": e.to(torch.uint8),
-            "cols": c.shape[1]}
+    e = torch.nn.functional.pad(e.to(torch.uint8), (0, scale_bytes(c.shape[1]) - e.shape[1]))
+    return {"codes": code[:, :, 0] | (code[:, :, 1] << 4), "scales": e, "cols": c.shape[1]}
 
 
 def unpack(codes, scales, cols):
     """fp32 values of packed matrices (any dimensions in front)."""
-    k = torch.stack((codes & 15, codes >> 4), -1).view(*scales.shape, BLOCK).to(torch.int32)
+    k = torch.stack((codes & 15, codes >> 4), -1).to(torch.int32).flatten(-2)
+    k = k.unflatten(-1, (-1, BLOCK))
     half = (k & 1).float() * 0.5
     mag = torch.where((k & 6) == 0, half, (1.0 + half) * power_of_two(126 + ((k & 6) >> 1)))
     v = torch.where(k > 7, -mag, mag)
-    e = scales.to(torch.int32)
+    e = scales[..., :k.shape[-2]].to(torch.int32)
     v = v * torch.where(e == 255, math.nan, power_of_two(e.clamp(max=254)))[..., None]
     return v.flatten(-2)[..., :cols]
 
@@ -389,7 +396,7 @@ def meaning(codes, scales, cols):
     for half in (0, 1):
         code = (codes >> (4 * half)) & 15
         out[:, half::2] = table[(code & 7).long()] * (1.0 - 2.0 * (code >> 3).double())
-    scale = torch.exp2(scales.double() - 127.0)
+    scale = torch.exp2(scales[:, :out.shape[1] // BLOCK].double() - 127.0)
     return (out * scale.repeat_interleave(BLOCK, 1))[:, :cols]
 
 
