@@ -12,7 +12,9 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libob_adam.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("ob_kernels.hip", "ob_adam.hip",
-                                            "ob_adamw_kernels.hip", "ob_adamw.hip")]
+                                            "ob_adamw_kernels.hip", "ob_adamw.hip",
+                                            "ob_mx4_kernels.hip", "ob_mx4_product.hip",
+                                            "ob_mx4.hip")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off",
          "-fhip-fp32-correctly-rounded-divide-sqrt", "-fno-gpu-flush-denormals-to-zero",

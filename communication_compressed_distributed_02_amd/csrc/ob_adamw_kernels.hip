@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "ob_adamw_kernels.h"
+#include "ob_random.h"
 
 namespace ob {
 namespace adamw {
@@ -82,30 +83,6 @@ __device__ __forceinline__ f32x4 load_some(const T* p, int n) {
   for (int k = 0; k < 4; ++k)
     if (k < n) r[k] = widen(p[k]);
   return r;
-}
-
-// Random bits: a 32-bit word hashed from the quad's index and the step's
-// first key, and more words from the word before and the second key.  The
-// multipliers are digits of sqrt(5), sqrt(3) and the golden ratio; every
-// input bit flips every output bit with probability 1/2 within the noise of
-// 65536 quads, and no two bits of the four words correlate above it.
-__device__ __forceinline__ uint32_t first_word(uint32_t quad, uint32_t key) {
-  uint32_t h = quad ^ key;
-  h = (h ^ (h >> 16)) * 0x3C6EF373u;
-  h = (h ^ (h >> 15)) * 0xBB67AE85u;
-  return h ^ (h >> 16);
-}
-__device__ __forceinline__ uint32_t next_word(uint32_t word, uint32_t key, uint32_t i) {
-  const uint32_t h = (word ^ key) * 0x9E3779B9u + i;
-  return h ^ (h >> 15);
-}
-// Quads past 2^32 take another key.
-__device__ __forceinline__ uint32_t high_key(uint64_t quad, uint32_t key) {
-  return key ^ ((uint32_t)(quad >> 32) * 0x9E3779B9u);
-}
-__device__ __forceinline__ uint32_t random16(uint32_t a, uint32_t b, int k) {
-  const uint32_t w = k < 2 ? a : b;
-  return k & 1 ? w >> 16 : w & 0xffffu;
 }
 
 // The low 16 bits of x's fp32 pattern rounded stochastically away.  What is
@@ -675,11 +652,6 @@ __global__ void __launch_bounds__(kBlock)
   if (norm != nullptr) *norm = (float)(sqrt(total) * (double)grad_scale);
 }
 
-__device__ __forceinline__ uint64_t mix64(uint64_t z, uint64_t mul) {
-  z ^= z >> 31;
-  return z * mul;
-}
-
 // What a step does with S: the clipping factor, the bias corrections and the
 // keys of its random bits, from the counts before it.
 struct Derived {
@@ -699,13 +671,9 @@ __device__ __forceinline__ Derived derive(const ControlArgs& a, double total, in
   if (a.max_norm > 0.0f && !(d.norm <= (double)a.max_norm)) coef = (double)a.max_norm / d.norm;
   d.gscale = (float)((double)a.grad_scale * coef);
   d.rbc2 = (float)(1.0 / sqrt(1.0 - d.p2));
-  // the multipliers are digits of the square roots of 2, 3 and 5
-  uint64_t z = a.seed * 0x6A09E667F3BCC909ull + (uint64_t)(steps + 1) * 0xBB67AE8584CAA73Bull;
-  z = mix64(z, 0x3C6EF372FE94F82Bull);
-  z = mix64(z, 0x6A09E667F3BCC909ull);
-  z ^= z >> 32;
-  d.k0 = (uint32_t)z;
-  d.k1 = (uint32_t)(z >> 32);
+  const Keys k = keys_of(a.seed, (uint64_t)(steps + 1));
+  d.k0 = k.k0;
+  d.k1 = k.k1;
   return d;
 }
 // The factors of group i.  A NaN rate becomes the canonical one: stochastic

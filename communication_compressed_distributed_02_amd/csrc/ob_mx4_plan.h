@@ -1,0 +1,158 @@
+// The host side's arithmetic behind the ob_mx4 C interface: validation, the
+// layout of quantised matrices and the choice of a product's kernel.  No HIP
+// in it, so that it is tested on its own.
+#pragma once
+
+#include <stdint.h>
+
+#include "ob_mx4.h"
+
+namespace ob {
+namespace mx4 {
+
+constexpr int kBlockElems = 32;   // elements of one scale
+constexpr int kPadElems = 128;    // a row of codes is padded to so many elements
+constexpr int kScalePad = 16;     // and a row of scales to so many bytes
+constexpr int kMaxMessages = OB_MX4_MAX_MESSAGES;
+constexpr int64_t kMaxElems = int64_t(1) << 40;  // of padded rows; no size below can overflow
+constexpr int64_t kMaxK = int64_t(1) << 24;      // 255 rows of k / 2 bytes stay below 2^32
+constexpr int64_t kMaxDim = int64_t(1) << 30;    // rows and columns of a product
+
+constexpr int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+constexpr int64_t padded(int64_t cols) { return up(cols, kPadElems); }
+constexpr int64_t row_codes(int64_t cols) { return padded(cols) / 2; }
+constexpr int64_t row_scales(int64_t cols) { return up(cols, kBlockElems * kScalePad) / kBlockElems; }
+inline uint64_t size_of(int32_t dtype) { return dtype == OB_MX4_BF16 ? 2 : 4; }
+
+inline bool aligned(const void* p, uintptr_t bytes) { return ((uintptr_t)p & (bytes - 1)) == 0; }
+inline bool dtype(int32_t v) { return v == OB_MX4_F32 || v == OB_MX4_BF16; }
+inline bool flag(int32_t v) { return v == 0 || v == 1; }
+
+// Rows and columns that a quantised matrix may have, in that order.
+inline bool shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxElems || cols > kMaxElems) return false;
+  return rows == 0 || row_scales(cols) * kBlockElems <= kMaxElems / rows;
+}
+
+// A stride that keeps every offset of rows x cols elements below 2^60.
+inline bool stride(int64_t rows, int64_t least, int64_t s) {
+  return s >= least && (rows <= 1 || s <= (int64_t(1) << 58) / rows);
+}
+
+// Memory that a call reads or writes; empty where it is null.
+struct Range {
+  uintptr_t begin, end;
+  bool written;
+};
+inline Range range(const void* p, uint64_t bytes, bool written) {
+  return {(uintptr_t)p, (uintptr_t)p + (p != nullptr ? bytes : 0), written};
+}
+inline uint64_t strided_bytes(int64_t rows, int64_t cols, int64_t s, int32_t type) {
+  return rows == 0 || cols == 0 ? 0 : ((uint64_t)(rows - 1) * s + cols) * size_of(type);
+}
+template <int N>
+inline bool disjoint(const Range (&r)[N]) {
+  for (int i = 0; i < N; ++i)
+    for (int j = 0; j < i; ++j)
+      if ((r[i].written || r[j].written) && r[i].begin < r[j].end && r[j].begin < r[i].end &&
+          r[i].begin < r[i].end && r[j].begin < r[j].end)
+        return false;
+  return true;
+}
+
+inline ob_status check_quantize(const ob_mx4_quantize_args* a) {
+  if (a == nullptr || !dtype(a->dtype) || !flag(a->stochastic)) return OB_ERR_ARG;
+  if (!shape(a->rows, a->cols) || (a->codes_t != nullptr && !shape(a->cols, a->rows)))
+    return OB_ERR_SHAPE;
+  if (!stride(a->rows, 0, a->stride)) return OB_ERR_ARG;
+  if ((a->codes == nullptr) != (a->scales == nullptr) ||
+      (a->codes_t == nullptr) != (a->scales_t == nullptr))
+    return OB_ERR_ARG;
+  if (a->rows == 0 || a->cols == 0) return OB_OK;
+  if (a->codes == nullptr && a->codes_t == nullptr) return OB_ERR_ARG;
+  if (a->x == nullptr || !aligned(a->x, size_of(a->dtype))) return OB_ERR_ARG;
+  if (a->residual != nullptr && (a->codes_t != nullptr || !aligned(a->residual, 4)))
+    return OB_ERR_ARG;
+  if (!aligned(a->seed_device, 8) || !aligned(a->codes, 16) || !aligned(a->scales, 16) ||
+      !aligned(a->codes_t, 16) || !aligned(a->scales_t, 16))
+    return OB_ERR_ARG;
+  const Range r[] = {
+      range(a->x, strided_bytes(a->rows, a->cols, a->stride, a->dtype), false),
+      range(a->seed_device, 8, false),
+      range(a->residual, (uint64_t)a->rows * a->cols * 4, true),
+      range(a->codes, (uint64_t)a->rows * row_codes(a->cols), true),
+      range(a->scales, (uint64_t)a->rows * row_scales(a->cols), true),
+      range(a->codes_t, (uint64_t)a->cols * row_codes(a->rows), true),
+      range(a->scales_t, (uint64_t)a->cols * row_scales(a->rows), true)};
+  return disjoint(r) ? OB_OK : OB_ERR_ARG;
+}
+
+inline ob_status check_average(const void* const* codes, const void* const* scales, int32_t n,
+                               int64_t rows, int64_t cols, int32_t type, const void* out,
+                               int64_t s) {
+  if (codes == nullptr || scales == nullptr || !dtype(type)) return OB_ERR_ARG;
+  if (n < 1 || n > kMaxMessages || !shape(rows, cols)) return OB_ERR_SHAPE;
+  if (!stride(rows, cols, s)) return OB_ERR_ARG;
+  if (rows == 0 || cols == 0) return OB_OK;
+  if (out == nullptr || !aligned(out, size_of(type))) return OB_ERR_ARG;
+  const Range o = range(out, strided_bytes(rows, cols, s, type), true);
+  for (int32_t i = 0; i < n; ++i) {
+    if (codes[i] == nullptr || scales[i] == nullptr || !aligned(codes[i], 16) ||
+        !aligned(scales[i], 16))
+      return OB_ERR_ARG;
+    const Range r[] = {o, range(codes[i], (uint64_t)rows * row_codes(cols), false),
+                       range(scales[i], (uint64_t)rows * row_scales(cols), false)};
+    if (!disjoint(r)) return OB_ERR_ARG;
+  }
+  return OB_OK;
+}
+
+// How a product is computed, from its sizes alone.
+struct Product {
+  bool empty;              // nothing to compute
+  uint64_t ws_bytes;
+};
+
+inline ob_status plan_product(const ob_mx4_matmul_args* a, Product* out) {
+  if (a == nullptr || !dtype(a->out_dtype) || !flag(a->accumulate)) return OB_ERR_ARG;
+  const bool packed = a->a_codes != nullptr || a->a_scales != nullptr;
+  if (!packed && !dtype(a->a_dtype)) return OB_ERR_ARG;
+  if (a->m < 0 || a->n < 0 || a->k < 0 || a->m > kMaxDim || a->n > kMaxDim || a->k > kMaxK ||
+      !shape(a->m, a->k) || !shape(a->n, a->k) || !shape(a->m, a->n))
+    return OB_ERR_SHAPE;
+  *out = Product{};
+  out->empty = a->m == 0 || a->n == 0;
+  return OB_OK;
+}
+
+inline ob_status check_product(const ob_mx4_matmul_args* a, const Product& p) {
+  if (!stride(a->m, a->n, a->out_stride)) return OB_ERR_ARG;
+  const bool packed = a->a_codes != nullptr || a->a_scales != nullptr;
+  if (!packed && !stride(a->m, 0, a->a_stride)) return OB_ERR_ARG;
+  if (p.empty) return OB_OK;
+  if (a->out == nullptr || !aligned(a->out, size_of(a->out_dtype))) return OB_ERR_ARG;
+  if (a->k > 0) {
+    if (packed ? a->a != nullptr || a->a_codes == nullptr || a->a_scales == nullptr ||
+                     !aligned(a->a_codes, 16) || !aligned(a->a_scales, 16)
+               : a->a == nullptr || !aligned(a->a, size_of(a->a_dtype)))
+      return OB_ERR_ARG;
+    if (a->b_codes == nullptr || a->b_scales == nullptr || !aligned(a->b_codes, 16) ||
+        !aligned(a->b_scales, 16))
+      return OB_ERR_ARG;
+  }
+  if (p.ws_bytes > 0 &&
+      (a->workspace == nullptr || !aligned(a->workspace, 256) || a->ws_bytes < p.ws_bytes))
+    return OB_ERR_WORKSPACE;
+  const Range r[] = {
+      range(a->a_codes, (uint64_t)a->m * row_codes(a->k), false),
+      range(a->a_scales, (uint64_t)a->m * row_scales(a->k), false),
+      range(a->a, strided_bytes(a->m, a->k, a->a_stride, a->a_dtype), false),
+      range(a->b_codes, (uint64_t)a->n * row_codes(a->k), false),
+      range(a->b_scales, (uint64_t)a->n * row_scales(a->k), false),
+      range(a->out, strided_bytes(a->m, a->n, a->out_stride, a->out_dtype), true),
+      range(a->workspace, p.ws_bytes, true)};
+  return disjoint(r) ? OB_OK : OB_ERR_ARG;
+}
+
+}  // namespace mx4
+}  // namespace ob

@@ -1,0 +1,417 @@
+"""Python binding of the ob_mx4 interface: matrices in microscaled 4-bit
+floating point (blocks of 32 elements that share a power of two), their
+products, and a linear layer made of them.
+
+    q = quantize(x)                     # x: float32 or bfloat16, blocks along its last dimension
+    rows, cols = quantize_both(x)       # x and its transpose, from one read
+    q.dequantize()                      # back to float32 or bfloat16
+    msg = quantize(g, seed=t, residual=e)      # a worker's message, with error feedback
+    mean = average(messages)            # of several workers
+    y = matmul(a, b)                    # a b^T on the matrix cores; a may be a plain tensor
+    y = linear(x, weight, seed=t)       # differentiable; all three products in 4 bits
+
+Functions work on the current stream of their tensors' device, as torch's own
+do, and may be captured in a graph.  They raise ValueError on tensors that do
+not fit and ObAdamError on a status other than OB_OK.  Every computation runs
+in the library's HIP kernels; there is no fallback.
+"""
+import ctypes
+
+import torch
+
+from .ob_adam import _check, _lib
+
+OB_MX4_F32, OB_MX4_BF16 = 0, 1
+OB_MX4_MAX_MESSAGES = 64
+
+EXPORTED = ("ob_mx4_layout", "ob_mx4_quantize", "ob_mx4_average", "ob_mx4_matmul_workspace",
+            "ob_mx4_matmul")
+
+_TYPES = {torch.float32: OB_MX4_F32, torch.bfloat16: OB_MX4_BF16}
+# the caller's current stream as a number (see ob_adamw)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+class ob_mx4_quantize_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("stochastic", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("stride", ctypes.c_int64),
+                ("seed", ctypes.c_uint64), ("seed_device", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("codes_t", ctypes.c_void_p),
+                ("scales_t", ctypes.c_void_p)]
+
+
+class ob_mx4_matmul_args(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a_codes", ctypes.c_void_p), ("a_scales", ctypes.c_void_p),
+                ("a", ctypes.c_void_p), ("a_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("a_stride", ctypes.c_int64), ("b_codes", ctypes.c_void_p),
+                ("b_scales", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("accumulate", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("ws_bytes", ctypes.c_uint64)]
+
+
+def _declare(L):
+    P, I32, I64, U64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
+    ptrs, i64s = ctypes.POINTER(P), ctypes.POINTER(I64)
+    product = ctypes.POINTER(ob_mx4_matmul_args)
+    sig = {
+        "ob_mx4_layout": [I64, I64, i64s, i64s],
+        "ob_mx4_quantize": [ctypes.POINTER(ob_mx4_quantize_args), P],
+        "ob_mx4_average": [ptrs, ptrs, I32, I64, I64, I32, P, I64, P],
+        "ob_mx4_matmul_workspace": [product, ctypes.POINTER(U64)],
+        "ob_mx4_matmul": [product, P],
+    }
+    for name, args in sig.items():
+        f = getattr(L, name)
+        f.argtypes = args
+        f.restype = ctypes.c_int
+
+
+_declare(_lib)
+
+
+def ob_mx4_layout(rows, cols):
+    """Bytes of (a row of codes, a row of scales)."""
+    codes, scales = ctypes.c_int64(0), ctypes.c_int64(0)
+    _check(_lib.ob_mx4_layout(rows, cols, ctypes.byref(codes), ctypes.byref(scales)),
+           "ob_mx4_layout")
+    return codes.value, scales.value
+
+
+def ob_mx4_quantize(args, stream_ptr):
+    _check(_lib.ob_mx4_quantize(ctypes.byref(args), stream_ptr), "ob_mx4_quantize")
+
+
+def ob_mx4_average(code_ptrs, scale_ptrs, rows, cols, dtype, out_ptr, stride, stream_ptr):
+    n = len(code_ptrs)
+    _check(_lib.ob_mx4_average((ctypes.c_void_p * n)(*code_ptrs), (ctypes.c_void_p * n)(*scale_ptrs),
+                               n, rows, cols, dtype, out_ptr, stride, stream_ptr),
+           "ob_mx4_average")
+
+
+def ob_mx4_matmul_workspace(args):
+    out = ctypes.c_uint64(0)
+    _check(_lib.ob_mx4_matmul_workspace(ctypes.byref(args), ctypes.byref(out)),
+           "ob_mx4_matmul_workspace")
+    return out.value
+
+
+def ob_mx4_matmul(args, stream_ptr):
+    _check(_lib.ob_mx4_matmul(ctypes.byref(args), stream_ptr), "ob_mx4_matmul")
+
+
+def _on(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            fn(*args, _current_stream(device.index))
+    else:
+        fn(*args, _current_stream(device.index))
+
+
+def _need_gpu(t, what):
+    if t.device.type != "cuda":
+        raise ValueError("%s on %s: a GPU is needed" % (what, t.device))
+
+
+class MX4:
+    """A quantised matrix: `codes` and `scales` as uint8 matrices in the layout
+    of include/ob_mx4.h, and its number of columns.  The tensors are taken as
+    they are, not copied."""
+    __slots__ = ("codes", "scales", "rows", "cols", "device")
+
+    def __init__(self, codes, scales, cols):
+        for t, what in ((codes, "codes"), (scales, "scales")):
+            if t.dtype != torch.uint8 or t.dim() != 2 or not t.is_contiguous():
+                raise ValueError("%s must be a contiguous uint8 matrix" % what)
+            _need_gpu(t, what)
+            if t.data_ptr() % 16:
+                raise ValueError("%s must be aligned to 16 bytes" % what)
+        width = ob_mx4_layout(codes.shape[0], cols)
+        if (codes.shape[1], scales.shape[1]) != width or scales.shape[0] != codes.shape[0]:
+            raise ValueError("codes %s and scales %s are not those of %d columns"
+                             % (tuple(codes.shape), tuple(scales.shape), cols))
+        if codes.device != scales.device:
+            raise ValueError("codes on %s, scales on %s" % (codes.device, scales.device))
+        self.codes, self.scales = codes, scales
+        self.rows, self.cols, self.device = codes.shape[0], cols, codes.device
+
+    @classmethod
+    def empty(cls, rows, cols, device):
+        """One with undefined contents."""
+        c, s = ob_mx4_layout(rows, cols)
+        return cls(torch.empty((rows, c), dtype=torch.uint8, device=device),
+                   torch.empty((rows, s), dtype=torch.uint8, device=device), cols)
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + self.scales.numel()
+
+    def dequantize(self, dtype=torch.float32, out=None):
+        """Its values as float32 or bfloat16."""
+        return average((self,), dtype, out)
+
+    def __repr__(self):
+        return "MX4(%d x %d on %s)" % (self.rows, self.cols, self.device)
+
+
+def _matrix(x, what):
+    """x as a matrix (dimensions in front of the last joined; a vector is one row)."""
+    if x.dtype not in _TYPES:
+        raise ValueError("%s must be float32 or bfloat16, not %s" % (what, x.dtype))
+    _need_gpu(x, what)
+    if x.dim() == 2:
+        return x
+    if x.dim() == 0:
+        raise ValueError("%s must have a dimension" % what)
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    try:
+        return x.view(rows, x.shape[-1])
+    except RuntimeError:
+        raise ValueError("%s of shape %s and strides %s is no matrix: make it contiguous"
+                         % (what, tuple(x.shape), x.stride())) from None
+
+
+def _by_rows(x):
+    return x.stride(1) == 1 or x.shape[1] <= 1
+
+
+def _row_stride(x):
+    """Elements between rows (of a single row any will do)."""
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _target(out, rows, cols, device, what):
+    if out is None:
+        return MX4.empty(rows, cols, device)
+    if out.shape != (rows, cols) or out.device != device:
+        raise ValueError("%s must be %d x %d on %s, not %r" % (what, rows, cols, device, out))
+    return out
+
+
+def _quantize(x, seed, residual, rows, cols):
+    """x by rows; rows: the MX4 of x or None, cols: that of its transpose or None."""
+    a = ob_mx4_quantize_args()
+    a.x, a.dtype = x.data_ptr(), _TYPES[x.dtype]
+    a.rows, a.cols, a.stride = x.shape[0], x.shape[1], _row_stride(x)
+    if seed is not None:
+        a.stochastic = 1
+        if isinstance(seed, torch.Tensor):
+            if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != x.device:
+                raise ValueError("a seed is a number or an int64 scalar on %s" % x.device)
+            a.seed_device = seed.data_ptr()
+        else:
+            a.seed = seed & 0xFFFFFFFFFFFFFFFF
+    if residual is not None:
+        a.residual = residual.data_ptr()
+    if rows is not None:
+        a.codes, a.scales = rows.codes.data_ptr(), rows.scales.data_ptr()
+    if cols is not None:
+        a.codes_t, a.scales_t = cols.codes.data_ptr(), cols.scales.data_ptr()
+    _on(x.device, ob_mx4_quantize, a)
+
+
+def quantize(x, seed=None, residual=None, out=None):
+    """The MX4 of x (float32 or bfloat16), in blocks along its last dimension;
+    dimensions in front of it are joined.  One dimension of the matrix has to be
+    contiguous, either one.
+
+    seed: round stochastically with these random bits (a number, or an int64
+    device scalar that is read when the call runs); None rounds to nearest.
+    residual: contiguous float32 of x's shape, added to x and replaced by what the
+    rounding left (error feedback).  out: an MX4 to write to."""
+    m = _matrix(x, "x")
+    flip = not _by_rows(m)
+    if flip and m.stride(0) != 1 and m.shape[0] > 1:
+        raise ValueError("x has strides %s: one dimension must be contiguous" % (m.stride(),))
+    if residual is not None:
+        if (residual.dtype != torch.float32 or residual.shape != x.shape
+                or residual.device != x.device or not residual.is_contiguous()):
+            raise ValueError("the residual must be a contiguous float32 tensor of x's shape on %s"
+                             % x.device)
+        if flip:
+            raise ValueError("with a residual, x must be contiguous along its last dimension")
+    out = _target(out, m.shape[0], m.shape[1], x.device, "out")
+    if flip:
+        _quantize(m.t(), seed, None, None, out)
+    else:
+        _quantize(m, seed, residual, out, None)
+    return out
+
+
+def quantize_both(x, seed=None, out=None):
+    """(quantize(x), quantize(x.t())) of a matrix, from one read.  out: a pair to
+    write to."""
+    m = _matrix(x, "x")
+    flip = not _by_rows(m)
+    if flip and m.stride(0) != 1 and m.shape[0] > 1:
+        raise ValueError("x has strides %s: one dimension must be contiguous" % (m.stride(),))
+    rows, cols = (None, None) if out is None else out
+    rows = _target(rows, m.shape[0], m.shape[1], x.device, "the first of out")
+    cols = _target(cols, m.shape[1], m.shape[0], x.device, "the second of out")
+    if flip:
+        _quantize(m.t(), seed, None, cols, rows)
+    else:
+        _quantize(m, seed, None, rows, cols)
+    return rows, cols
+
+
+def _result(out, rows, cols, dtype, device):
+    """The tensor that a call writes: `out` checked, or a new one."""
+    if dtype not in _TYPES:
+        raise ValueError("results are float32 or bfloat16, not %s" % dtype)
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    if (tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != device
+            or not _by_rows(out) or (rows > 1 and out.stride(0) < cols)):
+        raise ValueError("out must be %d x %d of %s on %s, rows contiguous and apart"
+                         % (rows, cols, dtype, device))
+    return out
+
+
+def average(messages, dtype=torch.float32, out=None):
+    """The mean of 1 to 64 MX4 of one shape, as float32 or bfloat16."""
+    messages = tuple(messages)
+    if not messages:
+        raise ValueError("no messages")
+    first = messages[0]
+    for q in messages:
+        if q.shape != first.shape or q.device != first.device:
+            raise ValueError("messages differ: %r and %r" % (first, q))
+    out = _result(out, first.rows, first.cols, dtype, first.device)
+    _on(first.device, ob_mx4_average, [q.codes.data_ptr() for q in messages],
+        [q.scales.data_ptr() for q in messages], first.rows, first.cols, _TYPES[dtype],
+        out.data_ptr(), _row_stride(out))
+    return out
+
+
+def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
+    """a b^T: a is M x K, b N x K, the result M x N of float32 or bfloat16.
+
+    b: an MX4.  a: an MX4, or a float32 or bfloat16 tensor, which is quantised
+    to nearest on the way (its dimensions in front of the last are those of the
+    result).  out: a matrix to write to; accumulate: add to it."""
+    args = ob_mx4_matmul_args()
+    if isinstance(a, MX4):
+        shape, rows, cols = None, a.rows, a.cols
+        args.a_codes, args.a_scales = a.codes.data_ptr(), a.scales.data_ptr()
+    else:
+        m = _matrix(a, "a")
+        if not _by_rows(m):
+            raise ValueError("a has strides %s: its last dimension must be contiguous"
+                             % (m.stride(),))
+        shape, rows, cols = a.shape[:-1], m.shape[0], m.shape[1]
+        args.a, args.a_dtype, args.a_stride = m.data_ptr(), _TYPES[m.dtype], _row_stride(m)
+    if cols != b.cols or a.device != b.device:
+        raise ValueError("a of %d columns on %s, b %r" % (cols, a.device, b))
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    c = _result(out, rows, b.rows, dtype, b.device)
+    args.m, args.n, args.k = rows, b.rows, cols
+    args.b_codes, args.b_scales = b.codes.data_ptr(), b.scales.data_ptr()
+    args.out, args.out_dtype, args.out_stride = c.data_ptr(), _TYPES[dtype], _row_stride(c)
+    args.accumulate = bool(accumulate)
+    need = ob_mx4_matmul_workspace(args)
+    if need:
+        # freed to torch's allocator on return: later work of this stream may have it then
+        scratch = torch.empty(need, dtype=torch.uint8, device=b.device)
+        args.workspace, args.ws_bytes = scratch.data_ptr(), need
+    _on(b.device, ob_mx4_matmul, args)
+    if out is None and shape is not None and len(shape) != 1:
+        return c.view(*shape, b.rows)
+    return c
+
+
+class Weight:
+    """A weight's 4-bit copies: `rows` (N x K) for the forward product, `cols` (K x N)
+    for the gradient of the input."""
+    __slots__ = ("rows", "cols", "version")
+
+    def __init__(self, weight):
+        self.rows, self.cols = quantize_both(weight.detach())
+        self.version = 0
+
+    def refresh(self, weight):
+        """Written again, where they lie, from the weight as it is now."""
+        quantize_both(weight.detach(), out=(self.rows, self.cols))
+        self.version += 1
+        return self
+
+
+def _unit(x):
+    """x as a matrix that quantize_both takes (a copy where it has to be)."""
+    m = x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x
+    return m if _by_rows(m) or m.stride(0) == 1 else m.contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, quantized, seed):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        m = _unit(x)
+        if quantized is None:
+            if need_x:
+                w, ctx.w_cols = quantize_both(weight)
+            else:
+                w = quantize(weight)
+        else:
+            w, ctx.version = quantized.rows, quantized.version
+            if need_x:
+                ctx.w_cols = quantized.cols
+        ctx.quantized = quantized
+        if need_w:
+            a, ctx.x_cols = quantize_both(m)
+        else:
+            a = m if _by_rows(m) else quantize(m)
+        ctx.seed, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = seed, x.shape, x.dtype, weight.dtype
+        return matmul(a, w, x.dtype).view(*x.shape[:-1], weight.shape[0])
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need_x, need_w = ctx.needs_input_grad[:2]
+        if ctx.quantized is not None and ctx.quantized.version != ctx.version:
+            raise RuntimeError("the weight's copies were refreshed between forward and backward")
+        dy = _unit(dy)
+        dx = dw = None
+        if need_x and need_w:
+            g, g_cols = quantize_both(dy, ctx.seed)
+        elif need_x:
+            g = quantize(dy, ctx.seed)
+        elif need_w:
+            g_cols = quantize(dy.t(), ctx.seed)
+        if need_x:
+            dx = matmul(g, ctx.w_cols, ctx.x_dtype).view(ctx.x_shape)
+        if need_w:
+            dw = matmul(g_cols, ctx.x_cols, ctx.w_dtype)
+        return dx, dw, None, None
+
+
+def linear(x, weight, quantized=None, seed=None):
+    """x weight^T with its gradients, all three products of 4-bit matrices:
+    y = Q(x) Q(w)^T, dx = Q(dy) Q(w^T)^T, dw = Q(dy^T) Q(x^T)^T.
+
+    x: [..., K], weight: [N, K], float32 or bfloat16; y and dx have x's type, dw
+    weight's.  quantized: the weight's copies where they are kept (a Weight of it,
+    as AdamWOptimizer keeps; they are not checked against it).  seed: round dy
+    stochastically, as quantize; None rounds it to nearest.  What the backward pass
+    keeps of x are 4-bit columns.  Not differentiable twice."""
+    if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x of shape %s, weight of shape %s" % (tuple(x.shape), tuple(weight.shape)))
+    if x.device != weight.device:
+        raise ValueError("x on %s, weight on %s" % (x.device, weight.device))
+    for t, what in ((x, "x"), (weight, "weight")):
+        if t.dtype not in _TYPES:
+            raise ValueError("%s must be float32 or bfloat16, not %s" % (what, t.dtype))
+        _need_gpu(t, what)
+    if quantized is not None and quantized.rows.shape != tuple(weight.shape):
+        raise ValueError("quantized is of a weight of %d x %d" % quantized.rows.shape)
+    return _Linear.apply(x, weight, quantized, seed)
