@@ -96,9 +96,27 @@ ob_status ob_mx4_matmul(const ob_mx4_matmul_args* a, void* stream) {
   p.accumulate = a->accumulate;
   const bool out_bf16 = a->out_dtype == OB_MX4_BF16;
   if (a->k == 0) return status(mx::launch_product_empty(p, out_bf16, (hipStream_t)stream));
-  const mx::AType type = a->a_codes != nullptr ? mx::kAPacked
+  mx::AType type = a->a_codes != nullptr ? mx::kAPacked
                          : a->a_dtype == OB_MX4_BF16 ? mx::kABf16 : mx::kAF32;
-  return status(mx::launch_product_narrow(p, type, out_bf16, (hipStream_t)stream));
+  if (plan.quantize) {
+    mx::QuantizeArgs q{};
+    q.x = p.a;
+    q.codes = (uint8_t*)a->workspace;
+    q.scales = (uint8_t*)a->workspace + plan.a_scales;
+    q.rows = p.m;
+    q.cols = p.k;
+    q.stride = p.a_stride;
+    const hipError_t e = mx::launch_quantize_rows(q, type == mx::kABf16, false, (hipStream_t)stream);
+    if (e != hipSuccess) return OB_ERR_HIP;
+    p.a_codes = q.codes;
+    p.a_scales = q.scales;
+    type = mx::kAPacked;
+  }
+  if (plan.shape == mx::kNarrow)
+    return status(mx::launch_product_narrow(p, type, out_bf16, (hipStream_t)stream));
+  return status(mx::launch_product_tiles(p, plan.shape, plan.splits, plan.per_split,
+                                         (float*)((char*)a->workspace + plan.parts), out_bf16,
+                                         (hipStream_t)stream));
 }
 
 }  // extern "C"

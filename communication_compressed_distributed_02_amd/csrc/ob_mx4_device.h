@@ -17,6 +17,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // Wide accesses at the alignment of one element, which gfx950 takes.
 typedef f32x4 f32x4_at4 __attribute__((aligned(4)));
 typedef u32x4 u32x4_at2 __attribute__((aligned(2)));
+typedef u32x2 u32x2_at2 __attribute__((aligned(2)));
 
 struct bf16 {
   uint16_t bits;
@@ -91,6 +92,16 @@ __device__ __forceinline__ float scale_of(uint32_t byte) {
 }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ uint32_t largest8(const float* c) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = magnitude(c[i]);
+    top = w > top ? w : top;
+  }
+  return top;
+}
 
 // Codes of 8 consecutive elements, c times inv (a power of two; 0 for a block
 // that is not finite).

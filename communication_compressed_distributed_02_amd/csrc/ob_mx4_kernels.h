@@ -45,9 +45,13 @@ struct ProductArgs {
 };
 // a_type: how a is given.
 enum AType { kAPacked, kAF32, kABf16 };
-// Tiles of 32 rows of a by 32 rows of b, the sum split over a block's waves.
+// m <= kNarrowRows; an a that is not packed takes narrow_lds(m, k) <= kNarrowLds.
 hipError_t launch_product_narrow(const ProductArgs& p, AType a_type, bool out_bf16,
                                  hipStream_t stream);
+// Large tiles, packed a; each split takes per_split units of 256 elements (even
+// where there are several).  parts: splits * m * up(n, 4) floats where splits > 1.
+hipError_t launch_product_tiles(const ProductArgs& p, Shape shape, int splits, int per_split,
+                                float* parts, bool out_bf16, hipStream_t stream);
 // out = 0, or left as it is with accumulate.
 hipError_t launch_product_empty(const ProductArgs& p, bool out_bf16, hipStream_t stream);
 

@@ -91,13 +91,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
   for (int u = 0; u < U; ++u) {
     // groups come in blocks of 4 on a quad of lanes, so a quad goes together
     if (at[u].row >= a.rows) continue;
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = magnitude(c[u][i]);
-      top = w > top ? w : top;
-    }
-    const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(top));
+    const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(largest8(c[u])));
     const float inv = inverse_scale(byte);
     const int64_t g = at[u].group;
     const uint32_t codes =
@@ -172,13 +166,7 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(QuantizeArgs a
       *(u32x4*)&tile[lr * kWords + lane_col / 2] = w;
     }
     if (a.codes != nullptr) {
-      uint32_t top = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t w = magnitude(c[k]);
-        top = w > top ? w : top;
-      }
-      const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(top));
+      const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(largest8(c)));
       const float inv = inverse_scale(byte);
       if (row < a.rows) {
         const uint32_t codes =

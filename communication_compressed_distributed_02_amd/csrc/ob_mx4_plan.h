@@ -107,21 +107,74 @@ inline ob_status check_average(const void* const* codes, const void* const* scal
   return OB_OK;
 }
 
-// How a product is computed, from its sizes alone.
+// How a product is computed, from its sizes and types alone.
+enum Shape { kNarrow, kTiles128, kTiles256 };
 struct Product {
   bool empty;              // nothing to compute
-  uint64_t ws_bytes;
+  bool quantize;           // a is quantised into the workspace first
+  Shape shape;
+  int splits, per_split;   // of the sum, in units of 256 elements
+  uint64_t a_scales, parts, ws_bytes;  // places in the workspace (a's codes at 0)
 };
+
+constexpr int kNarrowRows = 64;           // rows of a that the narrow kernel takes at most
+constexpr int kNarrowLds = 48 * 1024;     // bytes of LDS for an a that it quantises itself
+inline int64_t narrow_lds(int64_t m, int64_t k) { return m * (padded(k) / 128 * 68 + 16); }
+
+// Tiles of 128 x 128 or 256 x 256, and into how many parts the sum goes: the
+// shortest by an estimate in ns, a round of tiles at a time.
+inline void choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
+  struct Cost {
+    Shape shape;
+    int64_t size, slots;     // edge of a tile, tiles that run at once
+    double unit, fixed;      // of a round: a unit's, and what comes before and after
+  };
+  static constexpr Cost kCosts[] = {{kTiles128, 128, 512, 1220.0, 3000.0},
+                                    {kTiles256, 256, 256, 1810.0, 5400.0}};
+  const int64_t units = (row_codes(k) + 127) / 128;
+  double best = 0.0;
+  for (const Cost& c : kCosts) {
+    const int64_t tiles = up(m, c.size) / c.size * (up(n, c.size) / c.size);
+    for (int splits = 1; splits <= 16; splits *= 2) {
+      const int64_t per = up((units + splits - 1) / splits, splits > 1 ? 2 : 1);
+      const int64_t real = (units + per - 1) / per;
+      if (splits > 1 && (real < splits || tiles * splits > c.slots)) break;
+      const double rounds = (double)((tiles * real + c.slots - 1) / c.slots);
+      // a block that has its CU to itself is faster
+      const double alone = c.slots == 512 && tiles * real <= 256 ? 0.55 : 1.0;
+      double t = rounds * ((double)per * c.unit * alone + c.fixed);
+      if (real > 1) t += 3000.0 + (double)(m * n) * (real * 8.0 + 2.0) / 4000.0;
+      if (best == 0.0 || t < best) {
+        best = t;
+        p->shape = c.shape;
+        p->splits = (int)real;
+        p->per_split = (int)per;
+      }
+    }
+  }
+}
 
 inline ob_status plan_product(const ob_mx4_matmul_args* a, Product* out) {
   if (a == nullptr || !dtype(a->out_dtype) || !flag(a->accumulate)) return OB_ERR_ARG;
   const bool packed = a->a_codes != nullptr || a->a_scales != nullptr;
   if (!packed && !dtype(a->a_dtype)) return OB_ERR_ARG;
-  if (a->m < 0 || a->n < 0 || a->k < 0 || a->m > kMaxDim || a->n > kMaxDim || a->k > kMaxK ||
-      !shape(a->m, a->k) || !shape(a->n, a->k) || !shape(a->m, a->n))
+  const int64_t m = a->m, n = a->n, k = a->k;
+  if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxK || !shape(m, k) ||
+      !shape(n, k) || !shape(m, n))
     return OB_ERR_SHAPE;
   *out = Product{};
-  out->empty = a->m == 0 || a->n == 0;
+  out->empty = m == 0 || n == 0;
+  if (out->empty || k == 0) return OB_OK;
+  out->quantize = !packed && (m > kNarrowRows || narrow_lds(m, k) > kNarrowLds);
+  if (out->quantize) {
+    out->a_scales = up(m * row_codes(k), 256);
+    out->parts = out->a_scales + up(m * row_scales(k), 256);
+  }
+  out->ws_bytes = out->parts;
+  if (m > kNarrowRows) {
+    choose_tiles(m, n, k, out);
+    if (out->splits > 1) out->ws_bytes += (uint64_t)out->splits * m * up(n, 4) * 4;
+  }
   return OB_OK;
 }
 

@@ -84,11 +84,14 @@ def ob_mx4_quantize(args, stream_ptr):
     _check(_lib.ob_mx4_quantize(ctypes.byref(args), stream_ptr), "ob_mx4_quantize")
 
 
+_POINTERS = [ctypes.c_void_p * n for n in range(OB_MX4_MAX_MESSAGES + 2)]
+
+
 def ob_mx4_average(code_ptrs, scale_ptrs, rows, cols, dtype, out_ptr, stride, stream_ptr):
     n = len(code_ptrs)
-    _check(_lib.ob_mx4_average((ctypes.c_void_p * n)(*code_ptrs), (ctypes.c_void_p * n)(*scale_ptrs),
-                               n, rows, cols, dtype, out_ptr, stride, stream_ptr),
-           "ob_mx4_average")
+    array = _POINTERS[n] if n < len(_POINTERS) else ctypes.c_void_p * n
+    _check(_lib.ob_mx4_average(array(*code_ptrs), array(*scale_ptrs), n, rows, cols, dtype, out_ptr,
+                               stride, stream_ptr), "ob_mx4_average")
 
 
 def ob_mx4_matmul_workspace(args):
@@ -102,13 +105,22 @@ def ob_mx4_matmul(args, stream_ptr):
     _check(_lib.ob_mx4_matmul(ctypes.byref(args), stream_ptr), "ob_mx4_matmul")
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(device, fn, *args):
     """fn(*args, stream) with `device` current, on its current stream."""
-    if torch.cuda.current_device() != device.index:
+    if _current_device() != device.index:
         with torch.cuda.device(device):
             fn(*args, _current_stream(device.index))
     else:
         fn(*args, _current_stream(device.index))
+
+
+def _widths(cols):
+    """Bytes of a row of codes and of a row of scales (ob_mx4_layout, of sizes that
+    a tensor has already)."""
+    return (cols + 127) // 128 * 64, (cols + 511) // 512 * 16
 
 
 def _need_gpu(t, what):
@@ -120,7 +132,7 @@ class MX4:
     """A quantised matrix: `codes` and `scales` as uint8 matrices in the layout
     of include/ob_mx4.h, and its number of columns.  The tensors are taken as
     they are, not copied."""
-    __slots__ = ("codes", "scales", "rows", "cols", "device")
+    __slots__ = ("rows", "cols", "device", "code_ptr", "scale_ptr", "_held")
 
     def __init__(self, codes, scales, cols):
         for t, what in ((codes, "codes"), (scales, "scales")):
@@ -135,15 +147,44 @@ class MX4:
                              % (tuple(codes.shape), tuple(scales.shape), cols))
         if codes.device != scales.device:
             raise ValueError("codes on %s, scales on %s" % (codes.device, scales.device))
-        self.codes, self.scales = codes, scales
         self.rows, self.cols, self.device = codes.shape[0], cols, codes.device
+        self.code_ptr, self.scale_ptr = codes.data_ptr(), scales.data_ptr()
+        self._held = codes, scales
 
     @classmethod
     def empty(cls, rows, cols, device):
         """One with undefined contents."""
-        c, s = ob_mx4_layout(rows, cols)
-        return cls(torch.empty((rows, c), dtype=torch.uint8, device=device),
-                   torch.empty((rows, s), dtype=torch.uint8, device=device), cols)
+        ob_mx4_layout(rows, cols)
+        some = torch.empty(0, dtype=torch.uint8, device=device)
+        _need_gpu(some, "a quantised matrix")
+        return cls._like(some, rows, cols)
+
+    @classmethod
+    def _like(cls, x, rows, cols):
+        """One with undefined contents where the tensor x lies: codes and scales
+        in one allocation, made views of when they are asked for."""
+        q = object.__new__(cls)
+        c, s = _widths(cols)
+        held = x.new_empty(rows * (c + s), dtype=torch.uint8)
+        q.rows, q.cols, q.device, q._held = rows, cols, held.device, held
+        q.code_ptr = held.data_ptr()
+        q.scale_ptr = q.code_ptr + rows * c
+        return q
+
+    def _part(self, i):
+        if isinstance(self._held, tuple):
+            return self._held[i]
+        width = _widths(self.cols)
+        begin = i * self.rows * width[0]
+        return self._held[begin:begin + self.rows * width[i]].view(self.rows, width[i])
+
+    @property
+    def codes(self):
+        return self._part(0)
+
+    @property
+    def scales(self):
+        return self._part(1)
 
     @property
     def shape(self):
@@ -151,7 +192,7 @@ class MX4:
 
     @property
     def nbytes(self):
-        return self.codes.numel() + self.scales.numel()
+        return self.rows * sum(_widths(self.cols))
 
     def dequantize(self, dtype=torch.float32, out=None):
         """Its values as float32 or bfloat16."""
@@ -189,34 +230,30 @@ def _row_stride(x):
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
-def _target(out, rows, cols, device, what):
+def _target(out, rows, cols, x, what):
     if out is None:
-        return MX4.empty(rows, cols, device)
-    if out.shape != (rows, cols) or out.device != device:
-        raise ValueError("%s must be %d x %d on %s, not %r" % (what, rows, cols, device, out))
+        return MX4._like(x, rows, cols)
+    if out.rows != rows or out.cols != cols or out.device != x.device:
+        raise ValueError("%s must be %d x %d on %s, not %r" % (what, rows, cols, x.device, out))
     return out
 
 
 def _quantize(x, seed, residual, rows, cols):
     """x by rows; rows: the MX4 of x or None, cols: that of its transpose or None."""
-    a = ob_mx4_quantize_args()
-    a.x, a.dtype = x.data_ptr(), _TYPES[x.dtype]
-    a.rows, a.cols, a.stride = x.shape[0], x.shape[1], _row_stride(x)
-    if seed is not None:
-        a.stochastic = 1
-        if isinstance(seed, torch.Tensor):
-            if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != x.device:
-                raise ValueError("a seed is a number or an int64 scalar on %s" % x.device)
-            a.seed_device = seed.data_ptr()
-        else:
-            a.seed = seed & 0xFFFFFFFFFFFFFFFF
-    if residual is not None:
-        a.residual = residual.data_ptr()
-    if rows is not None:
-        a.codes, a.scales = rows.codes.data_ptr(), rows.scales.data_ptr()
-    if cols is not None:
-        a.codes_t, a.scales_t = cols.codes.data_ptr(), cols.scales.data_ptr()
-    _on(x.device, ob_mx4_quantize, a)
+    m, n = x.shape
+    device = x.device
+    where = None
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != device:
+            raise ValueError("a seed is a number or an int64 scalar on %s" % device)
+        where = seed.data_ptr()
+    a = ob_mx4_quantize_args(
+        x.data_ptr(), _TYPES[x.dtype], seed is not None, m, n, x.stride(0) if m > 1 else n,
+        0 if seed is None or where is not None else seed & 0xFFFFFFFFFFFFFFFF, where,
+        None if residual is None else residual.data_ptr(), None if rows is None else rows.code_ptr,
+        None if rows is None else rows.scale_ptr, None if cols is None else cols.code_ptr,
+        None if cols is None else cols.scale_ptr)
+    _on(device, ob_mx4_quantize, a)
 
 
 def quantize(x, seed=None, residual=None, out=None):
@@ -239,7 +276,7 @@ def quantize(x, seed=None, residual=None, out=None):
                              % x.device)
         if flip:
             raise ValueError("with a residual, x must be contiguous along its last dimension")
-    out = _target(out, m.shape[0], m.shape[1], x.device, "out")
+    out = _target(out, m.shape[0], m.shape[1], x, "out")
     if flip:
         _quantize(m.t(), seed, None, None, out)
     else:
@@ -255,8 +292,8 @@ def quantize_both(x, seed=None, out=None):
     if flip and m.stride(0) != 1 and m.shape[0] > 1:
         raise ValueError("x has strides %s: one dimension must be contiguous" % (m.stride(),))
     rows, cols = (None, None) if out is None else out
-    rows = _target(rows, m.shape[0], m.shape[1], x.device, "the first of out")
-    cols = _target(cols, m.shape[1], m.shape[0], x.device, "the second of out")
+    rows = _target(rows, m.shape[0], m.shape[1], x, "the first of out")
+    cols = _target(cols, m.shape[1], m.shape[0], x, "the second of out")
     if flip:
         _quantize(m.t(), seed, None, cols, rows)
     else:
@@ -269,7 +306,7 @@ def _result(out, rows, cols, dtype, device):
     if dtype not in _TYPES:
         raise ValueError("results are float32 or bfloat16, not %s" % dtype)
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
     if (tuple(out.shape) != (rows, cols) or out.dtype != dtype or out.device != device
             or not _by_rows(out) or (rows > 1 and out.stride(0) < cols)):
         raise ValueError("out must be %d x %d of %s on %s, rows contiguous and apart"
@@ -283,12 +320,12 @@ def average(messages, dtype=torch.float32, out=None):
     if not messages:
         raise ValueError("no messages")
     first = messages[0]
-    for q in messages:
-        if q.shape != first.shape or q.device != first.device:
+    for q in messages[1:]:
+        if q.rows != first.rows or q.cols != first.cols or q.device != first.device:
             raise ValueError("messages differ: %r and %r" % (first, q))
     out = _result(out, first.rows, first.cols, dtype, first.device)
-    _on(first.device, ob_mx4_average, [q.codes.data_ptr() for q in messages],
-        [q.scales.data_ptr() for q in messages], first.rows, first.cols, _TYPES[dtype],
+    _on(first.device, ob_mx4_average, [q.code_ptr for q in messages],
+        [q.scale_ptr for q in messages], first.rows, first.cols, _TYPES[dtype],
         out.data_ptr(), _row_stride(out))
     return out
 
@@ -299,33 +336,33 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
     b: an MX4.  a: an MX4, or a float32 or bfloat16 tensor, which is quantised
     to nearest on the way (its dimensions in front of the last are those of the
     result).  out: a matrix to write to; accumulate: add to it."""
-    args = ob_mx4_matmul_args()
     if isinstance(a, MX4):
-        shape, rows, cols = None, a.rows, a.cols
-        args.a_codes, args.a_scales = a.codes.data_ptr(), a.scales.data_ptr()
+        shape, rows, cols, device = None, a.rows, a.cols, a.device
+        given = a.code_ptr, a.scale_ptr, None, 0
+        stride = 0
     else:
         m = _matrix(a, "a")
         if not _by_rows(m):
             raise ValueError("a has strides %s: its last dimension must be contiguous"
                              % (m.stride(),))
-        shape, rows, cols = a.shape[:-1], m.shape[0], m.shape[1]
-        args.a, args.a_dtype, args.a_stride = m.data_ptr(), _TYPES[m.dtype], _row_stride(m)
-    if cols != b.cols or a.device != b.device:
-        raise ValueError("a of %d columns on %s, b %r" % (cols, a.device, b))
+        (rows, cols), device = m.shape, m.device
+        shape = a.shape[:-1]
+        given = None, None, m.data_ptr(), _TYPES[m.dtype]
+        stride = m.stride(0) if rows > 1 else cols
+    if cols != b.cols or device != b.device:
+        raise ValueError("a of %d columns on %s, b %r" % (cols, device, b))
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
-    c = _result(out, rows, b.rows, dtype, b.device)
-    args.m, args.n, args.k = rows, b.rows, cols
-    args.b_codes, args.b_scales = b.codes.data_ptr(), b.scales.data_ptr()
-    args.out, args.out_dtype, args.out_stride = c.data_ptr(), _TYPES[dtype], _row_stride(c)
-    args.accumulate = bool(accumulate)
+    c = _result(out, rows, b.rows, dtype, device)
+    args = ob_mx4_matmul_args(rows, b.rows, cols, *given, _TYPES[dtype], stride, b.code_ptr,
+                              b.scale_ptr, c.data_ptr(), _row_stride(c), bool(accumulate), None, 0)
     need = ob_mx4_matmul_workspace(args)
     if need:
         # freed to torch's allocator on return: later work of this stream may have it then
-        scratch = torch.empty(need, dtype=torch.uint8, device=b.device)
+        scratch = torch.empty(need, dtype=torch.uint8, device=device)
         args.workspace, args.ws_bytes = scratch.data_ptr(), need
-    _on(b.device, ob_mx4_matmul, args)
-    if out is None and shape is not None and len(shape) != 1:
+    _on(device, ob_mx4_matmul, args)
+    if shape is not None and len(shape) != 1 and out is None:
         return c.view(*shape, b.rows)
     return c
 

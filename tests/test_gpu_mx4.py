@@ -260,6 +260,46 @@ def test_product_of_integers_is_exact(mx, out, raw):
         assert (wide == 5.0).all()
 
 
+LARGE = [(65, 70, 5000), (70, 5000, 130), (300, 260, 8200), (2100, 2051, 300), (4101, 2051, 300),
+         (4101, 2051, 1100), (4096, 2048, 512), (4097, 2305, 129), (256, 256, 16384), (8193, 1031, 700)]
+
+
+@pytest.mark.parametrize("raw", [None, "bf16"])
+def test_large_products_of_integers_are_exact(mx, raw):
+    """Sizes that take each shape of tile, whole and at its edges, one unit of
+    the sum, an odd half of one, and sums in several parts."""
+    for i, (m, n, k) in enumerate(LARGE):
+        a, b = gpu(integers(m, k, i)), gpu(integers(n, k, 50 + i))
+        want = a.double() @ b.double().t()
+        qa = mx.quantize(a) if raw is None else a.to(DT[raw])
+        qb = mx.quantize(b)
+        for dtype in (torch.float32, torch.bfloat16):
+            wide = torch.full((m + 2, n + 3), 5.0, dtype=dtype, device="cuda")
+            part = wide[1:m + 1, 2:n + 2]
+            mx.matmul(qa, qb, dtype, out=part)
+            assert torch.equal(part, want.to(dtype)), (m, n, k)
+            part.copy_(want)
+            two = (want + part.double()).to(dtype)
+            mx.matmul(qa, qb, dtype, out=part, accumulate=True)
+            assert torch.equal(part, two), (m, n, k)
+            part.fill_(5.0)
+            assert (wide == 5.0).all()
+        log("%d x %d x %d" % (m, n, k))
+
+
+@pytest.mark.parametrize("m, n, k", [(300, 300, 4000), (4097, 2305, 1200), (40, 700, 3000)])
+def test_large_products_of_spread_values(mx, m, n, k):
+    x, w = gpu(ref.spread(m, k, 1)), gpu(ref.spread(n, k, 2))
+    qx, qw = mx.quantize(x), mx.quantize(w)
+    a, b = qx.dequantize().double(), qw.dequantize().double()
+    first = mx.matmul(qx, qw, torch.float32)
+    off = (first.double() - a @ b.t()).abs()
+    assert (off <= k * 2.0 ** -23 * (a.abs() @ b.abs().t())).all()
+    for _ in range(2):
+        assert torch.equal(first, mx.matmul(qx, qw, torch.float32))
+    assert torch.equal(first, mx.matmul(x, qw, torch.float32))
+
+
 def product_bound(a, b):
     """k additions, each off by at most a step of the sum of magnitudes so far
     (2^-23, should the matrix cores cut instead of rounding)."""

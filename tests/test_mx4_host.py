@@ -135,6 +135,70 @@ def test_matmul_refusals(mx):
                                  b_scales=None), None)
 
 
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("shim") / "libmx4plan.so")
+    subprocess.check_call(
+        ["g++", "-std=c++17", "-O1", "-g", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC",
+         "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-static-libubsan",
+         "-I", os.path.join(ROOT, "include"),
+         "-I", os.path.join(ROOT, "communication_compressed_distributed_02_amd", "csrc"),
+         os.path.join(ROOT, "tests", "c_abi", "mx4_plan_shim.cpp"), "-o", so])
+    L = ctypes.CDLL(so)
+    L.shim_narrow_lds.restype = ctypes.c_int64
+    return L
+
+
+def test_products_are_planned_within_their_limits(mx, shim):
+    """Every plan covers the sum once, gives the kernels what they assume and
+    takes a workspace of the parts' size."""
+    r = np.random.default_rng(1)
+    sizes = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000, 1600, 4096,
+             6400, 16384, 1 << 20, 1 << 24]
+    cases = [tuple(r.choice(sizes, 3)) for _ in range(3000)] + [(1 << 30, 1, 1), (1, 1 << 30, 1),
+                                                               (1, 1, 1 << 24), (64, 64, 1 << 24)]
+    for m, n, k in cases:
+        m, n, k = int(m), int(n), int(k)
+        for raw in (False, True):
+            kw = dict(a_codes=None, a_scales=None, a=place(5), a_stride=k) if raw else {}
+            a = matmul_args(mx, m=m, n=n, k=k, out_stride=n, **kw)
+            out = (ctypes.c_int64 * 8)()
+            st = shim.shim_plan(ctypes.byref(a), out)
+            if max(m, n) * 512 * -(-k // 512) > 1 << 40 or m * 512 * -(-n // 512) > 1 << 40:
+                assert st != 0
+                continue
+            assert st == 0
+            empty, quantize, shape, splits, per, a_scales, parts, ws = out
+            lds = shim.shim_narrow_lds(ctypes.c_int64(m), ctypes.c_int64(k))
+            assert not empty and (shape == 0) == (m <= 64)
+            assert quantize == (raw and (m > 64 or lds > 48 * 1024))
+            if quantize:
+                codes, scales = ref.widths(k)
+                assert a_scales % 256 == 0 and a_scales >= m * codes
+                assert parts % 256 == 0 and parts >= a_scales + m * scales
+            else:
+                assert parts == 0
+            if shape:
+                units = -(-k // 256)
+                assert splits >= 1 and per >= 1 and (splits - 1) * per < units <= splits * per
+                assert splits == 1 or per % 2 == 0
+                assert splits <= 65535
+                assert ws == parts + (splits * m * (-(-n // 4) * 4) * 4 if splits > 1 else 0)
+            else:
+                assert ws == parts
+    # a workspace that is missing, misaligned, short or overlapped
+    big = dict(m=300, n=300, k=4096, out_stride=300, a_codes=None, a_scales=None, a=place(5),
+               a_stride=4096)
+    need = mx.ob_mx4_matmul_workspace(matmul_args(mx, **big))
+    assert need > 300 * 2048
+    for kw in (dict(workspace=None, ws_bytes=need), dict(workspace=place(6) + 16, ws_bytes=need),
+               dict(workspace=place(6), ws_bytes=need - 1)):
+        refused(mx, lambda: mx.ob_mx4_matmul(matmul_args(mx, **big, **kw), None), "WORKSPACE")
+    for where in (place(4), place(5) - 256, place(2)):
+        refused(mx, lambda: mx.ob_mx4_matmul(
+            matmul_args(mx, **big, workspace=where, ws_bytes=need), None), "ARG")
+
+
 def test_tensors_off_the_gpu_are_refused(mx):
     x = torch.ones(4, 64)
     for call in (lambda: mx.quantize(x), lambda: mx.quantize_both(x), lambda: mx.linear(x, x),
