@@ -57,7 +57,7 @@ __device__ __forceinline__ Place place_of(Start s, int64_t rows, int64_t groups,
 }
 
 // Rows of x, 8 elements a lane.
-template <typename T, bool RESIDUAL, bool STOCHASTIC, int U>
+template <typename T, bool RESIDUAL, bool STOCHASTIC, bool WIDE, int U>
 __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a) {
   const int64_t groups = padded(a.cols) / kLaneElems;
   const int64_t rc = row_codes(a.cols), rs = row_scales(a.cols);
@@ -73,14 +73,14 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
     const int64_t col = at[u].group * kLaneElems;
     const T* x = (const T*)a.x + at[u].row * a.stride + col;
     if (col + kLaneElems <= a.cols)
-      load8(x, c[u]);
+      RESIDUAL ? load8_stream(x, c[u]) : load8(x, c[u]);
     else
       load8_some(x, (int)(a.cols > col ? a.cols - col : 0), c[u]);
     if (RESIDUAL) {
       float e[8];
       const float* r = a.residual + at[u].row * a.cols + col;
       if (col + kLaneElems <= a.cols)
-        load8(r, e);
+        load8_stream(r, e);
       else
         load8_some(r, (int)(a.cols > col ? a.cols - col : 0), e);
 #pragma unroll
@@ -91,13 +91,12 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
   for (int u = 0; u < U; ++u) {
     // groups come in blocks of 4 on a quad of lanes, so a quad goes together
     if (at[u].row >= a.rows) continue;
-    const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(largest8(c[u])));
-    const float inv = inverse_scale(byte);
+    const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(largest<8>(c[u])));
     const int64_t g = at[u].group;
     const uint32_t codes =
-        STOCHASTIC
-            ? encode8_stochastic(c[u], inv, (uint64_t)(at[u].row * groups + g) * 2, keys)
-            : encode8(c[u], inv);
+        STOCHASTIC ? encode8_stochastic<WIDE>(c[u], byte, (uint64_t)(at[u].row * groups + g) * 2,
+                                              keys)
+                   : encode8(c[u], byte);
     *(uint32_t*)(a.codes + at[u].row * rc + g * 4) = codes;
     if ((threadIdx.x & 3) == 0) {
       uint8_t* scales = a.scales + at[u].row * rs;
@@ -113,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = c[u][i] - v[i];
       if (col + kLaneElems <= a.cols) {
-        store8(r, v);
+        store8_stream(r, v);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -124,137 +123,248 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
 }
 
 // The transposed matrix, and the rows too where codes is not null, from one
-// read: a block takes a tile of 128 x 128, quantises the rows on their way
-// into LDS, then every lane reads 32 elements down a column.  The transposed
-// codes go through LDS so that a column's 64 bytes are written together.
-constexpr int kTile = 128;
-template <typename T, bool STOCHASTIC>
-__global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(QuantizeArgs a) {
-  constexpr int kWords = kTile * (int)sizeof(T) / 4;      // 32-bit words of a tile's row
-  constexpr int kPerWord = 4 / (int)sizeof(T);            // columns in one of them
-  __shared__ __attribute__((aligned(16))) uint32_t tile[kTile * kWords];
-  __shared__ __attribute__((aligned(16))) u32x4 out[kTile * 4];
-  __shared__ uint8_t out_scale[kTile * 4];
-  const int64_t tiles_c = padded(a.cols) / kTile;
+// read: a wave holds 32 rows of 256 columns in registers, 4 columns a lane, so
+// that a block down a column lies on one lane and one along a row on 8.  The
+// transposed codes of 4 waves go through LDS to be written as 64 bytes of a
+// column, the scales of both as words.
+constexpr int kTileCols = 256, kTileWaves = 4, kTileRows = kTileWaves * kBlockElems;
+template <typename T>
+struct Four;  // 4 neighbouring elements
+template <>
+struct Four<float> {
+  f32x4 w;
+  __device__ __forceinline__ void clear() { w = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }
+  __device__ __forceinline__ void load(const float* p) { w = *(const f32x4_at4*)p; }
+  // The first n, 1 to 3.
+  __device__ __forceinline__ void load_some(const float* p, int n) {
+    w[0] = p[0];
+    if (n > 1) w[1] = p[1];
+    if (n > 2) w[2] = p[2];
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const float c[4] = {w[0], w[1], w[2], w[3]};
+    return largest<4>(c);
+  }
+  __device__ __forceinline__ uint32_t encode(uint32_t byte) const {
+    const float c[4] = {w[0], w[1], w[2], w[3]};
+    return encode4(c, byte);
+  }
+  template <bool WIDE>
+  __device__ __forceinline__ uint32_t stochastic(uint32_t byte, uint64_t quad, Keys k) const {
+    const float c[4] = {w[0], w[1], w[2], w[3]};
+    return encode4_stochastic<WIDE>(c, byte, quad, k);
+  }
+};
+template <>
+struct Four<bf16> {
+  u32x2 w;
+  __device__ __forceinline__ void clear() { w = u32x2{0u, 0u}; }
+  __device__ __forceinline__ void load(const bf16* p) { w = *(const u32x2_at2*)p; }
+  __device__ __forceinline__ void load_some(const bf16* p, int n) {
+    w[0] = p[0].bits;
+    if (n > 1) w[0] |= (uint32_t)p[1].bits << 16;
+    if (n > 2) w[1] = p[2].bits;
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    return larger(__builtin_elementwise_max(magnitudes(w[0]), magnitudes(w[1])));
+  }
+  __device__ __forceinline__ uint32_t encode(uint32_t byte) const { return encode4(w, byte); }
+  template <bool WIDE>
+  __device__ __forceinline__ uint32_t stochastic(uint32_t byte, uint64_t quad, Keys k) const {
+    return encode4_stochastic<WIDE>(w, byte, quad, k);
+  }
+};
+
+// Column j of 32 rows: its largest magnitude, and 8 of its codes at a time.
+__device__ __forceinline__ uint32_t column_top(const Four<float>* x, int j) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kBlockElems; ++i) {
+    const uint32_t w = magnitude(x[i].w[j]);
+    top = w > top ? w : top;
+  }
+  return top;
+}
+__device__ __forceinline__ uint32_t column_top(const Four<bf16>* x, int j) {
+  u16x2 top = magnitudes(x[0].w[j >> 1]);  // of two columns, once for both
+#pragma unroll
+  for (int i = 1; i < kBlockElems; ++i)
+    top = __builtin_elementwise_max(top, magnitudes(x[i].w[j >> 1]));
+  return (uint32_t)top[j & 1] << 16;
+}
+template <bool STOCHASTIC, bool WIDE>
+__device__ __forceinline__ uint32_t column_codes(const Four<float>* x, int j, uint32_t byte,
+                                                 uint64_t quad, Keys k) {
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = x[i].w[j];
+  return STOCHASTIC ? encode8_stochastic<WIDE>(c, byte, quad, k) : encode8(c, byte);
+}
+template <bool STOCHASTIC, bool WIDE>
+__device__ __forceinline__ uint32_t column_codes(const Four<bf16>* x, int j, uint32_t byte,
+                                                 uint64_t quad, Keys k) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // the low or the high halves of two rows
+    w[i] = __builtin_amdgcn_perm(x[2 * i + 1].w[j >> 1], x[2 * i].w[j >> 1],
+                                 j & 1 ? 0x07060302u : 0x05040100u);
+  return STOCHASTIC ? encode8_stochastic<WIDE>(w, byte, quad, k) : encode8(w, byte);
+}
+
+template <typename T, bool STOCHASTIC, bool WIDE>
+__global__ void __launch_bounds__(kTileWaves * 64) quantize_tiles_kernel(QuantizeArgs a) {
+  __shared__ __attribute__((aligned(16))) u32x4 out[kTileCols * kTileWaves];
+  __shared__ __attribute__((aligned(8))) uint8_t out_scale[kTileCols * kTileWaves];
+  __shared__ __attribute__((aligned(8))) uint8_t row_scale[kTileRows * 8];
+  const int64_t tiles_c = (a.cols + kTileCols - 1) / kTileCols;
   const int64_t tr = (int64_t)blockIdx.x / tiles_c, tc = (int64_t)blockIdx.x - tr * tiles_c;
-  const int64_t r0 = tr * kTile, c0 = tc * kTile;
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = (int)threadIdx.x & 63;
+  const int64_t r0 = tr * kTileRows + wave * kBlockElems, c0 = tc * kTileCols, col = c0 + lane * 4;
   const int64_t rc = row_codes(a.cols), rs = row_scales(a.cols);
   Keys keys{};
   if (STOCHASTIC) keys = call_keys(a);
-  const int tid = (int)threadIdx.x;
-  // 16 lanes take a row, 16 rows a round
-  const int lane_col = (tid & 15) * kLaneElems, lane_row = tid >> 4;
-#pragma unroll 4
-  for (int i = 0; i < kTile / 16; ++i) {
-    const int lr = i * 16 + lane_row;
-    const int64_t row = r0 + lr, col = c0 + lane_col;
-    float c[8];
-    if (row < a.rows && col + kLaneElems <= a.cols) {
-      load8((const T*)a.x + row * a.stride + col, c);
-    } else {
-      const int n = row < a.rows && col < a.cols ? (int)(a.cols - col) : 0;
-      load8_some((const T*)a.x + (n > 0 ? row * a.stride + col : 0), n, c);
-    }
-    if constexpr (sizeof(T) == 4) {
-      *(f32x4*)&tile[lr * kWords + lane_col] = f32x4{c[0], c[1], c[2], c[3]};
-      *(f32x4*)&tile[lr * kWords + lane_col + 4] = f32x4{c[4], c[5], c[6], c[7]};
-    } else {
-      u32x4 w;
+  Four<T> x[kBlockElems];
+  const int rows = (int)(a.rows - r0 < kBlockElems ? a.rows - r0 : kBlockElems);
+  const int64_t first_row = tr * kTileRows;
+  if (rows == kBlockElems && c0 + kTileCols <= a.cols) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[k] = (__float_as_uint(c[2 * k]) >> 16) | __float_as_uint(c[2 * k + 1]);
-      *(u32x4*)&tile[lr * kWords + lane_col / 2] = w;
-    }
-    if (a.codes != nullptr) {
-      const uint32_t byte = scale_byte<STOCHASTIC>(quad_max(largest8(c)));
-      const float inv = inverse_scale(byte);
-      if (row < a.rows) {
-        const uint32_t codes =
-            STOCHASTIC ? encode8_stochastic(c, inv, (uint64_t)(row * padded(a.cols) + col) / 4, keys)
-                       : encode8(c, inv);
-        *(uint32_t*)(a.codes + row * rc + col / 2) = codes;
-        if ((tid & 3) == 0) a.scales[row * rs + col / kBlockElems] = (uint8_t)byte;
-        if ((tid & 15) == 0 && tc == tiles_c - 1)
-          for (int64_t k = tiles_c * 4; k < rs; ++k) a.scales[row * rs + k] = 0;
-      }
+    for (int i = 0; i < kBlockElems; ++i) x[i].load((const T*)a.x + (r0 + i) * a.stride + col);
+  } else {
+    // at an edge: zeros where there are no elements
+#pragma unroll
+    for (int i = 0; i < kBlockElems; ++i) x[i].clear();
+    if (col + 4 <= a.cols) {
+#pragma unroll
+      for (int i = 0; i < kBlockElems; ++i)
+        if (i < rows) x[i].load((const T*)a.x + (r0 + i) * a.stride + col);
+    } else if (col < a.cols) {
+#pragma unroll
+      for (int i = 0; i < kBlockElems; ++i)
+        if (i < rows)
+          x[i].load_some((const T*)a.x + (r0 + i) * a.stride + col, (int)(a.cols - col));
     }
   }
-  __syncthreads();
+  if (a.codes != nullptr) {
+    const bool inside = col < padded(a.cols);
+#pragma unroll
+    for (int i = 0; i < kBlockElems; ++i) {
+      const uint32_t byte = scale_byte<STOCHASTIC>(oct_max(x[i].top()));
+      const uint64_t quad = (uint64_t)((r0 + i) * (padded(a.cols) / 4) + col / 4);
+      const uint32_t codes = STOCHASTIC ? x[i].template stochastic<WIDE>(byte, quad, keys)
+                                        : x[i].encode(byte);
+      if (i < rows && inside) *(uint16_t*)(a.codes + (r0 + i) * rc + col / 2) = (uint16_t)codes;
+      if ((lane & 7) == 0) row_scale[(wave * kBlockElems + i) * 8 + lane / 8] = (uint8_t)byte;
+      // few rows at a time, so that the registers do
+      if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  // The values are taken apart again from here on: kept from the rows they would
+  // take twice the registers.
+#pragma unroll
+  for (int i = 0; i < kBlockElems; ++i) asm volatile("" : "+v"(x[i].w));
   const int64_t trc = row_codes(a.rows), trs = row_scales(a.rows);
-  const int64_t tiles_r = padded(a.rows) / kTile;
-  constexpr int kTasks = kWords * 4;  // words across the tile, times blocks down it
 #pragma unroll
-  for (int t = 0; t < kTasks / kThreads; ++t) {
-    const int word = (tid + t * kThreads) % kWords, block = (tid + t * kThreads) / kWords;
-    uint32_t w[kBlockElems];
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t byte = scale_byte<STOCHASTIC>(column_top(x, j));
+    const uint64_t quad = (uint64_t)((col + j) * (padded(a.rows) / 4) + r0 / 4);
+    u32x4 codes;
 #pragma unroll
-    for (int i = 0; i < kBlockElems; ++i) w[i] = tile[(block * kBlockElems + i) * kWords + word];
-#pragma unroll
-    for (int p = 0; p < kPerWord; ++p) {
-      float c[kBlockElems];
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < kBlockElems; ++i) {
-        const uint32_t bits = kPerWord == 1 ? w[i] : p == 0 ? w[i] << 16 : w[i] & 0xffff0000u;
-        c[i] = __uint_as_float(bits);
-        top = (bits & 0x7fffffffu) > top ? bits & 0x7fffffffu : top;
-      }
-      const uint32_t byte = scale_byte<STOCHASTIC>(top);
-      const float inv = inverse_scale(byte);
-      const int lc = word * kPerWord + p;
-      u32x4 codes;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint64_t at = (uint64_t)((c0 + lc) * padded(a.rows) + r0 + block * kBlockElems) / 4;
-        codes[k] = STOCHASTIC ? encode8_stochastic(c + 8 * k, inv, at + 2 * k, keys)
-                              : encode8(c + 8 * k, inv);
-      }
-      out[lc * 4 + block] = codes;
-      out_scale[lc * 4 + block] = (uint8_t)byte;
-    }
+    for (int k = 0; k < 4; ++k)
+      codes[k] = column_codes<STOCHASTIC, WIDE>(x + 8 * k, j, byte, quad + 2 * k, keys);
+    // lanes that write together are 4 columns apart: each to a place of its own
+    out[(lane * 4 + j) * kTileWaves + (wave ^ (lane & (kTileWaves - 1)))] = codes;
+    out_scale[(lane * 4 + j) * kTileWaves + wave] = (uint8_t)byte;
+    __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 #pragma unroll
-  for (int t = 0; t < kTile * 4 / kThreads; ++t) {
-    const int i = t * kThreads + tid, lc = i >> 2, piece = i & 3;
-    const int64_t row = c0 + lc;
-    if (row >= a.cols) continue;
-    *(u32x4*)(a.codes_t + row * trc + r0 / 2 + piece * 16) = out[i];
-    a.scales_t[row * trs + r0 / kBlockElems + piece] = out_scale[i];
-    if (piece == 0 && tr == tiles_r - 1)
-      for (int64_t k = tiles_r * 4; k < trs; ++k) a.scales_t[row * trs + k] = 0;
+  for (int t = 0; t < kTileCols / 64; ++t) {
+    const int i = t * kTileWaves * 64 + (int)threadIdx.x, lc = i / kTileWaves, piece = i % kTileWaves;
+    const int64_t at = first_row / 2 + piece * 16;
+    if (c0 + lc < a.cols && at < trc)
+      *(u32x4*)(a.codes_t + (c0 + lc) * trc + at) =
+          out[lc * kTileWaves + (piece ^ (lc / 4 & (kTileWaves - 1)))];
+  }
+  // scales in words of 4; those of rows that do not exist are zero, and the last
+  // tile's go on to the end of the padding
+  const int64_t tiles_r = (a.rows + kTileRows - 1) / kTileRows;
+  for (int i = (int)threadIdx.x; i < kTileCols * kTileWaves / 4; i += kTileWaves * 64) {
+    const int lc = i / (kTileWaves / 4), part = i % (kTileWaves / 4);
+    const int64_t at = first_row / kBlockElems + part * 4;
+    if (c0 + lc >= a.cols) continue;
+    uint8_t* to = a.scales_t + (c0 + lc) * trs;
+    if (at < trs) *(uint32_t*)(to + at) = *(const uint32_t*)&out_scale[lc * kTileWaves + part * 4];
+    if (part == 0 && tr == tiles_r - 1)
+      for (int64_t k = tiles_r * kTileWaves; k < trs; k += 4) *(uint32_t*)(to + k) = 0;
+  }
+  if (a.codes != nullptr) {
+    for (int i = (int)threadIdx.x; i < kTileRows * 2; i += kTileWaves * 64) {
+      const int64_t row = first_row + i / 2, at = c0 / kBlockElems + (i & 1) * 4;
+      if (row >= a.rows) continue;
+      uint8_t* to = a.scales + row * rs;
+      if (at < rs) *(uint32_t*)(to + at) = *(const uint32_t*)&row_scale[i * 4];
+      if ((i & 1) == 0 && tc == tiles_c - 1)
+        for (int64_t k = tiles_c * 8; k < rs; k += 4) *(uint32_t*)(to + k) = 0;
+    }
   }
 }
 
-// Mean of n messages, 8 elements a lane.
+// Mean of n messages, 8 elements a lane; the loads of kAhead messages at a time.
+constexpr int kAhead = 8;
 template <typename T, int U>
 __global__ void __launch_bounds__(kThreads) average_kernel(AverageArgs a) {
   const int64_t groups = padded(a.cols) / kLaneElems;
   const int64_t rc = row_codes(a.cols), rs = row_scales(a.cols);
   const Start s = start_of((int64_t)blockIdx.x * (kThreads * U), a.rows, groups);
+  Place at[U];
+  int64_t code_at[U], scale_at[U];
+  float sum[U][8];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const Place at = place_of(s, a.rows, groups, u * kThreads + threadIdx.x);
-    const int64_t col = at.group * kLaneElems;
-    if (at.row >= a.rows || col >= a.cols) continue;
-    float sum[8];
-    for (int i = 0; i < a.n; ++i) {
-      const uint32_t codes = *(const uint32_t*)(a.codes[i] + at.row * rc + at.group * 4);
-      const float scale = scale_of(a.scales[i][at.row * rs + at.group / 4]);
-      float v[8];
-      decode8(codes, scale, v);
+    at[u] = place_of(s, a.rows, groups, u * kThreads + threadIdx.x);
+    // lanes behind the last row or column read what the first lane of all does
+    const bool inside = at[u].row < a.rows && at[u].group * kLaneElems < a.cols;
+    code_at[u] = inside ? at[u].row * rc + at[u].group * 4 : 0;
+    scale_at[u] = inside ? at[u].row * rs + at[u].group / 4 : 0;
+    if (!inside) at[u].row = a.rows;
+  }
+  for (int i0 = 0; i0 < a.n; i0 += kAhead) {
+    uint32_t codes[kAhead][U], bytes[kAhead][U];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] = i == 0 ? v[k] : sum[k] + v[k];
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.n) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        codes[i][u] = *(const uint32_t*)(a.codes[i0 + i] + code_at[u]);
+        bytes[i][u] = a.scales[i0 + i][scale_at[u]];
+      }
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] *= a.factor;
-    T* out = (T*)a.out + at.row * a.stride + col;
+    for (int i = 0; i < kAhead; ++i) {
+      if (i0 + i >= a.n) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float v[8];
+        decode8(codes[i][u], scale_of(bytes[i][u]), v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[u][k] = i0 + i == 0 ? v[k] : sum[u][k] + v[k];
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (at[u].row >= a.rows) continue;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum[u][k] *= a.factor;
+    const int64_t col = at[u].group * kLaneElems;
+    T* out = (T*)a.out + at[u].row * a.stride + col;
     if (col + kLaneElems <= a.cols) {
-      store8(out, sum);
+      store8(out, sum[u]);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (col + k < a.cols) store1(out + k, sum[k]);
+        if (col + k < a.cols) store1(out + k, sum[u][k]);
     }
   }
 }
@@ -267,39 +377,51 @@ int64_t blocks_for(int64_t rows, int64_t cols, int64_t per) {
 // and more stay below it.
 constexpr int kUnroll = 2;
 
-template <typename T, bool STOCHASTIC>
+// Whether the index of four elements of rows x cols, padded, may pass 2^32.
+bool wide(int64_t rows, int64_t cols) { return rows * (padded(cols) / 4) > int64_t(1) << 32; }
+
+template <typename T, bool STOCHASTIC, bool WIDE>
 hipError_t quantize_rows(const QuantizeArgs& a, hipStream_t stream) {
   const dim3 grid((uint32_t)blocks_for(a.rows, a.cols, kThreads * kUnroll));
   if (a.residual != nullptr)
-    quantize_rows_kernel<T, true, STOCHASTIC, kUnroll><<<grid, kThreads, 0, stream>>>(a);
+    quantize_rows_kernel<T, true, STOCHASTIC, WIDE, kUnroll><<<grid, kThreads, 0, stream>>>(a);
   else
-    quantize_rows_kernel<T, false, STOCHASTIC, kUnroll><<<grid, kThreads, 0, stream>>>(a);
+    quantize_rows_kernel<T, false, STOCHASTIC, WIDE, kUnroll><<<grid, kThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
+template <typename T>
+hipError_t quantize_rows(const QuantizeArgs& a, bool stochastic, hipStream_t stream) {
+  if (!stochastic) return quantize_rows<T, false, false>(a, stream);
+  return wide(a.rows, a.cols) ? quantize_rows<T, true, true>(a, stream)
+                              : quantize_rows<T, true, false>(a, stream);
+}
 
-template <typename T, bool STOCHASTIC>
+template <typename T, bool STOCHASTIC, bool WIDE>
 hipError_t quantize_tiles(const QuantizeArgs& a, hipStream_t stream) {
-  const dim3 grid((uint32_t)(padded(a.rows) / kTile * (padded(a.cols) / kTile)));
-  quantize_tiles_kernel<T, STOCHASTIC><<<grid, kThreads, 0, stream>>>(a);
+  const int64_t tr = (a.rows + kTileRows - 1) / kTileRows;
+  const dim3 grid((uint32_t)(tr * ((a.cols + kTileCols - 1) / kTileCols)));
+  quantize_tiles_kernel<T, STOCHASTIC, WIDE><<<grid, kTileWaves * 64, 0, stream>>>(a);
   return hipGetLastError();
+}
+template <typename T>
+hipError_t quantize_tiles(const QuantizeArgs& a, bool stochastic, hipStream_t stream) {
+  if (!stochastic) return quantize_tiles<T, false, false>(a, stream);
+  return wide(a.rows, a.cols) || wide(a.cols, a.rows) ? quantize_tiles<T, true, true>(a, stream)
+                                                      : quantize_tiles<T, true, false>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_quantize_rows(const QuantizeArgs& a, bool is_bf16, bool stochastic,
                                 hipStream_t stream) {
-  if (is_bf16)
-    return stochastic ? quantize_rows<bf16, true>(a, stream) : quantize_rows<bf16, false>(a, stream);
-  return stochastic ? quantize_rows<float, true>(a, stream) : quantize_rows<float, false>(a, stream);
+  return is_bf16 ? quantize_rows<bf16>(a, stochastic, stream)
+                 : quantize_rows<float>(a, stochastic, stream);
 }
 
 hipError_t launch_quantize_tiles(const QuantizeArgs& a, bool is_bf16, bool stochastic,
                                  hipStream_t stream) {
-  if (is_bf16)
-    return stochastic ? quantize_tiles<bf16, true>(a, stream)
-                      : quantize_tiles<bf16, false>(a, stream);
-  return stochastic ? quantize_tiles<float, true>(a, stream)
-                    : quantize_tiles<float, false>(a, stream);
+  return is_bf16 ? quantize_tiles<bf16>(a, stochastic, stream)
+                 : quantize_tiles<float>(a, stochastic, stream);
 }
 
 hipError_t launch_average(const AverageArgs& a, bool is_bf16, hipStream_t stream) {

@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
         load8(x, c);
       else
         load8_some(x, (int)(p.k > k ? p.k - k : 0), c);
-      const uint32_t byte = scale_byte<false>(quad_max(largest8(c)));
-      *(uint32_t*)(lds + r * lc + at * 4) = encode8(c, inverse_scale(byte));
+      const uint32_t byte = scale_byte<false>(quad_max(largest<8>(c)));
+      *(uint32_t*)(lds + r * lc + at * 4) = encode8(c, byte);
       lds_scales[r * ls + at / 4] = (uint8_t)byte;
     }
     __syncthreads();
@@ -219,12 +219,6 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
 // This wave's reads and loads are done, and so are those of all the block's waves.
 __device__ __forceinline__ void arrived() {
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-// What this wave wrote to LDS is there for all its lanes.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 // A uniform 64-bit value in scalar registers.
 __device__ __forceinline__ uint64_t uniform(uint64_t x) {

@@ -21,10 +21,11 @@ def keys(seed):
     return z & U32, z >> 32
 
 
-def noise(rows, cols, seed):
-    """16 random bits for every element of the padded matrix."""
+def noise(rows, cols, seed, first_row=0):
+    """16 random bits for every element of the padded matrix (from a row on)."""
     k0, k1 = keys(seed)
     quad = np.arange(rows * widths(cols)[0] // 2, dtype=np.uint64)
+    quad += np.uint64(first_row * widths(cols)[0] // 2)
     h = ((quad & U32) ^ np.uint64(k0)) ^ ((quad >> np.uint64(32)) * np.uint64(0x9E3779B9) & U32)
     h = (h ^ (h >> np.uint64(16))) * np.uint64(0x3C6EF373) & U32
     h = (h ^ (h >> np.uint64(15))) * np.uint64(0xBB67AE85) & U32
@@ -35,8 +36,9 @@ def noise(rows, cols, seed):
     return four.astype(np.float64).reshape(rows, -1)
 
 
-def quantize(c, seed=None):
-    """(codes, scales) of a matrix of fp32 values, as the library lays them out."""
+def quantize(c, seed=None, first_row=0):
+    """(codes, scales) of a matrix of fp32 values, as the library lays them out, or
+    of the rows from first_row on of a larger one."""
     c = np.asarray(c, dtype=np.float32)
     rows, cols = c.shape
     cb, sb = widths(cols)
@@ -47,7 +49,7 @@ def quantize(c, seed=None):
     sign[:, :cols] = np.signbit(c)
     index = np.zeros(wide.shape, dtype=np.uint8)
     scales = np.zeros((rows, sb), dtype=np.uint8)
-    u = None if seed is None else noise(rows, cols, seed)
+    u = None if seed is None else noise(rows, cols, seed, first_row)
     for b in range(cb // 16):
         part = slice(32 * b, 32 * b + 32)
         v = wide[:, part]

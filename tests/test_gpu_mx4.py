@@ -11,8 +11,9 @@ from gpu_common import log
 pytestmark = pytest.mark.gpu
 
 DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+# rows and columns on either side of blocks, of the padding and of a kernel's tile
 SIZES = [(1, 1), (1, 31), (2, 32), (3, 33), (1, 127), (5, 128), (2, 129), (3, 333), (7, 511),
-         (4, 513), (130, 257), (129, 1), (128, 128), (257, 100), (1, 9001), (33, 2048)]
+         (4, 513), (130, 257), (129, 1), (128, 128), (257, 100), (1, 9001), (33, 2048), (128, 256), (127, 258), (161, 767), (384, 514)]
 
 
 @pytest.fixture(scope="module")
@@ -29,8 +30,8 @@ def host(t):
     return t.detach().float().cpu().numpy()
 
 
-def assert_packed(q, c, seed=None, where=""):
-    codes, scales = ref.quantize(c, seed)
+def assert_packed(q, c, seed=None, where="", first_row=0):
+    codes, scales = ref.quantize(c, seed, first_row)
     got = q.scales.cpu().numpy()
     assert np.array_equal(got, scales), "%s scales differ at %s" % (
         where, np.argwhere(got != scales)[:4].tolist())
@@ -202,7 +203,7 @@ def test_error_feedback(mx, dtype, seed):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_average(mx, dtype):
-    for n, (rows, cols) in zip((1, 2, 3, 4, 7, 8, 9, 16, 17, 64, 5, 2, 33, 1, 4, 2), SIZES):
+    for n, (rows, cols) in zip((1, 2, 3, 4, 7, 8, 9, 16, 17, 64, 5, 2, 33, 1, 4, 2, 3, 9, 1, 8), SIZES):
         many = [mx.quantize(gpu(ref.spread(rows, cols, 50 + i)), seed=i) for i in range(n)]
         hosts = [ref.values(q.codes.cpu().numpy(), q.scales.cpu().numpy(), cols) for q in many]
         total = hosts[0].astype(np.float32)
@@ -497,6 +498,43 @@ def test_two_streams_at_once(mx):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_offsets_past_32_bits(mx):
+    """Rows whose elements, groups of four and bytes lie past 2^32, from an input
+    that is one row over and over."""
+    rows, cols = (1 << 24) + 6, 1024
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    x = gpu(ref.spread(1, cols, 1)).expand(rows, cols)
+    picks = [0, 1, (1 << 22) + 1, (1 << 23) - 1, (1 << 23) + 3, 1 << 24, (1 << 24) + 5]
+    q = mx.quantize(x, seed=9)
+    for r in picks:
+        # the definition over this row's own groups of four
+        codes, scales = ref.quantize(host(x[:1]), 9, first_row=r)
+        assert np.array_equal(q.codes[r].cpu().numpy(), codes[0]), r
+        assert np.array_equal(q.scales[r].cpu().numpy(), scales[0]), r
+    out = q.dequantize(torch.bfloat16)
+    for r in picks:
+        want = ref.values(q.codes[r:r + 1].cpu().numpy(), q.scales[r:r + 1].cpu().numpy(), cols)
+        assert np.array_equal(host(out[r:r + 1]), want.astype(np.float32)), r
+    del out
+    w = mx.quantize(gpu(integers(48, cols, 3)))
+    b = w.dequantize().double()
+    y = mx.matmul(q, w, torch.float32)
+    last = mx.MX4(q.codes[-600:], q.scales[-600:], cols)
+    assert torch.equal(y[-600:], mx.matmul(last, w, torch.float32))
+    few = mx.matmul(mx.MX4(w.codes[:3], w.scales[:3], cols), q, torch.float32)
+    a = last.dequantize().double()
+    off = (few[:, -600:].double() - b[:3] @ a.t()).abs()
+    assert (off <= cols * 2.0 ** -23 * (b[:3].abs() @ a.abs().t())).all()
+    del y, few, q
+    # the transposed matrix of a flat one is the tallest there is
+    flat = gpu(ref.spread(1, 1 << 22, 2))
+    a, b = mx.quantize_both(flat[:, :1 << 20], seed=4)
+    assert_packed(a, host(flat[:, :1 << 20]), 4)
+    assert_packed(mx.MX4(b.codes[-70:].contiguous(), b.scales[-70:].contiguous(), 1),
+                  host(flat[:, (1 << 20) - 70:1 << 20]).T, 4, first_row=(1 << 20) - 70)
 
 
 def test_refusals(mx):
