@@ -117,20 +117,26 @@ struct Product {
   uint64_t a_scales, parts, ws_bytes;  // places in the workspace (a's codes at 0)
 };
 
-constexpr int kNarrowRows = 64;           // rows of a that the narrow kernel takes at most
-constexpr int kNarrowLds = 48 * 1024;     // bytes of LDS for an a that it quantises itself
-inline int64_t narrow_lds(int64_t m, int64_t k) { return m * (padded(k) / 128 * 68 + 16); }
+constexpr int kNarrowRows = 64;        // rows of a that the narrow kernel takes at most
+constexpr int kNarrowLds = 32 * 1024;  // bytes of LDS that it uses at most
+// Elements of an a that it quantises itself, by every block: 16 rows of 1024
+// 4.4 us, 2.0 and 3.1 in two launches; 16 of 1600 8.2, and 2.0 and 4.4.
+constexpr int64_t kNarrowElems = 24 * 1024;
+inline int64_t narrow_lds(int64_t m, int64_t k) { return m * (padded(k) / 128 * 72 + 24); }
 
 // Tiles of 128 x 128 or 256 x 256, and into how many parts the sum goes: the
-// shortest by an estimate in ns, a round of tiles at a time.
-inline void choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
+// shortest by an estimate in ns, a round of tiles at a time.  The figures are
+// those of 8192 x 8192 x 16384 (both shapes) and of short sums; the choices
+// against all others, in us: 4096 x 1024 x 4096 15.6, next 26.1; 8192 x 8192 x
+// 16384 484, 631; 300 x 1000 x 16384 in 8 parts 17, 20 in 4, 37 in one.
+inline double choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
   struct Cost {
     Shape shape;
     int64_t size, slots;     // edge of a tile, tiles that run at once
     double unit, fixed;      // of a round: a unit's, and what comes before and after
   };
   static constexpr Cost kCosts[] = {{kTiles128, 128, 512, 1220.0, 3000.0},
-                                    {kTiles256, 256, 256, 1810.0, 5400.0}};
+                                    {kTiles256, 256, 256, 1810.0, 7000.0}};
   const int64_t units = (row_codes(k) + 127) / 128;
   double best = 0.0;
   for (const Cost& c : kCosts) {
@@ -152,6 +158,13 @@ inline void choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
       }
     }
   }
+  return best;
+}
+// What the narrow kernel takes: b's bytes at 4 TB/s, and more the more rows of a.
+// One row of 16384 x 16384 36 us (tiles 26), 16 rows 58 (28); of 4096 x 4096 4.4
+// (8.3) and 5.8 (9.5), 64 rows 11.1 (11.0).
+inline double narrow_time(int64_t m, int64_t n, int64_t k) {
+  return 2500.0 + (double)n * row_codes(k) * (0.246e-3 + 0.0124e-3 * m);
 }
 
 inline ob_status plan_product(const ob_mx4_matmul_args* a, Product* out) {
@@ -165,16 +178,18 @@ inline ob_status plan_product(const ob_mx4_matmul_args* a, Product* out) {
   *out = Product{};
   out->empty = m == 0 || n == 0;
   if (out->empty || k == 0) return OB_OK;
-  out->quantize = !packed && (m > kNarrowRows || narrow_lds(m, k) > kNarrowLds);
+  const double time = choose_tiles(m, n, k, out);
+  if (m <= kNarrowRows && narrow_time(m, n, k) <= time) {
+    out->shape = kNarrow;
+    out->splits = out->per_split = 0;
+  }
+  out->quantize = !packed && (out->shape != kNarrow || m * padded(k) > kNarrowElems);
   if (out->quantize) {
     out->a_scales = up(m * row_codes(k), 256);
     out->parts = out->a_scales + up(m * row_scales(k), 256);
   }
   out->ws_bytes = out->parts;
-  if (m > kNarrowRows) {
-    choose_tiles(m, n, k, out);
-    if (out->splits > 1) out->ws_bytes += (uint64_t)out->splits * m * up(n, 4) * 4;
-  }
+  if (out->splits > 1) out->ws_bytes += (uint64_t)out->splits * m * up(n, 4) * 4;
   return OB_OK;
 }
 

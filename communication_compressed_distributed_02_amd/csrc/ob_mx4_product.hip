@@ -81,13 +81,13 @@ __device__ __forceinline__ void write_out(T* row, int at, int64_t left, int32_t 
 }
 
 // Products with few rows of a (m <= 16 * MT), bound by reading b: a block takes 16
-// rows of b, its waves every kWaves-th unit of the sum, kAhead units of loads at
-// a time, and they add up through LDS in their order.  The instruction of 16
-// rows by 16 and 128 elements: lane l holds row l % 16, elements 32 * (l / 16)
-// to + 31 and their scale; of the results, row l % 16 of a and 4 * (l / 16) + i
-// of b.  An a that is not quantised is, by every block for itself, into LDS,
-// while its first loads of b are on their way.
-constexpr int kWaves = 8, kAhead = 4;
+// rows of b, its waves every kWaves-th 256 elements of the sum (lines of 128
+// bytes), kAhead of them in loads at a time, and they add up through LDS in their
+// order.  The instruction of 16 rows by 16 and 128 elements: lane l holds row
+// l % 16, elements 32 * (l / 16) to + 31 and their scale; of the results, row
+// l % 16 of a and 4 * (l / 16) + i of b.  An a that is not quantised is, by every
+// block for itself, into LDS, while its first loads of b are on their way.
+constexpr int kWaves = 8, kAhead = 2;
 template <int MT, AType A, typename T>
 __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -95,26 +95,27 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
   const int lane = (int)threadIdx.x & 63, row = lane & 15, block = lane >> 4;
   const int64_t rc = row_codes(p.k), rs = row_scales(p.k);
   const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int units = (int)(rc / 64);
+  const int units = (int)(rc / 64), pairs = (units + 1) / 2;  // of 128 elements, of 256
   // rows behind the last are read as the last, and their results dropped
   const int64_t bn = n0 + row < p.n ? n0 + row : p.n - 1;
   const uint8_t* b_codes = p.b_codes + bn * rc + block * 16;
-  const uint8_t* b_scales = p.b_scales + bn * rs + block;
-  u32x4 b[kAhead];
-  uint32_t sb[kAhead];
-  const auto load = [&](int u0) {
+  const uint8_t* b_scales = p.b_scales + bn * rs;
+  u32x4 b[kAhead][2];
+  u32x2 sb[kAhead];
+  const auto load = [&](int p0) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int u = u0 + i * kWaves;
-      if (u >= units) continue;
-      b[i] = *(const u32x4*)(b_codes + (int64_t)u * 64);
-      sb[i] = b_scales[(int64_t)u * 4];
+      const int at = p0 + i * kWaves;
+      if (at >= pairs) continue;
+      b[i][0] = *(const u32x4*)(b_codes + (int64_t)at * 128);
+      if (2 * at + 1 < units) b[i][1] = *(const u32x4*)(b_codes + (int64_t)at * 128 + 64);
+      sb[i] = *(const u32x2*)(b_scales + (int64_t)at * 8);
     }
   };
   load(wave);
   // rows of a in LDS: codes, 16 bytes apart so that rows start in other banks,
   // then the scales
-  const int lc = units * 64 + 16, ls = units * 4;
+  const int lc = units * 64 + 16, ls = pairs * 8;
   uint8_t* lds_scales = lds + (int)p.m * lc;
   if constexpr (A != kAPacked) {
     using X = typename Raw<A>::type;
@@ -141,24 +142,29 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-  for (int u0 = wave; u0 < units; u0 += kAhead * kWaves) {
-    if (u0 != wave) load(u0);
+  for (int p0 = wave; p0 < pairs; p0 += kAhead * kWaves) {
+    if (p0 != wave) load(p0);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int u = u0 + i * kWaves;
-      if (u >= units) continue;
+      const int at = p0 + i * kWaves;
+      if (at >= pairs) continue;
+      const bool two = 2 * at + 1 < units;
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        u32x4 a;
-        uint32_t sa;
+        const uint8_t *codes, *scales;
         if constexpr (A == kAPacked) {
-          a = *(const u32x4*)(p.a_codes + am[j] * rc + (int64_t)u * 64 + block * 16);
-          sa = p.a_scales[am[j] * rs + (int64_t)u * 4 + block];
+          codes = p.a_codes + am[j] * rc + (int64_t)at * 128 + block * 16;
+          scales = p.a_scales + am[j] * rs + (int64_t)at * 8;
         } else {
-          a = *(const u32x4*)(lds + am[j] * lc + u * 64 + block * 16);
-          sa = lds_scales[am[j] * ls + u * 4 + block];
+          codes = lds + am[j] * lc + at * 128 + block * 16;
+          scales = lds_scales + am[j] * ls + at * 8;
         }
-        acc[j] = multiply16(b[i], a, acc[j], sb[i], sa);
+        const u32x2 sa = *(const u32x2*)scales;
+        acc[j] = multiply16(b[i][0], *(const u32x4*)codes, acc[j], sb[i].x >> (8 * block),
+                            sa.x >> (8 * block));
+        if (two)
+          acc[j] = multiply16(b[i][1], *(const u32x4*)(codes + 64), acc[j], sb[i].y >> (8 * block),
+                              sa.y >> (8 * block));
       }
     }
   }

@@ -330,6 +330,21 @@ def average(messages, dtype=torch.float32, out=None):
     return out
 
 
+_needs = {}
+
+
+def _workspace(args, m, n, k, plain):
+    """ob_mx4_matmul_workspace, which goes by these alone, of sizes asked for
+    before."""
+    key = m, n, k, plain
+    need = _needs.get(key)
+    if need is None:
+        if len(_needs) >= 4096:
+            _needs.clear()
+        need = _needs[key] = ob_mx4_matmul_workspace(args)
+    return need
+
+
 def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
     """a b^T: a is M x K, b N x K, the result M x N of float32 or bfloat16.
 
@@ -356,7 +371,7 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
     c = _result(out, rows, b.rows, dtype, device)
     args = ob_mx4_matmul_args(rows, b.rows, cols, *given, _TYPES[dtype], stride, b.code_ptr,
                               b.scale_ptr, c.data_ptr(), _row_stride(c), bool(accumulate), None, 0)
-    need = ob_mx4_matmul_workspace(args)
+    need = _workspace(args, rows, b.rows, cols, args.a_codes is None)
     if need:
         # freed to torch's allocator on return: later work of this stream may have it then
         scratch = torch.empty(need, dtype=torch.uint8, device=device)

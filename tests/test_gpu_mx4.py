@@ -265,11 +265,15 @@ LARGE = [(65, 70, 5000), (70, 5000, 130), (300, 260, 8200), (2100, 2051, 300), (
          (4101, 2051, 1100), (4096, 2048, 512), (4097, 2305, 129), (256, 256, 16384), (8193, 1031, 700)]
 
 
+FEW = [(1, 6400, 1600), (4, 1600, 6400), (16, 17, 16384), (24, 1000, 1024), (25, 1000, 1024), (64, 33, 129),
+       (64, 1024, 4096), (64, 6000, 6000), (33, 16, 20000), (2, 9000, 9000)]
+
+
 @pytest.mark.parametrize("raw", [None, "bf16"])
 def test_large_products_of_integers_are_exact(mx, raw):
     """Sizes that take each shape of tile, whole and at its edges, one unit of
     the sum, an odd half of one, and sums in several parts."""
-    for i, (m, n, k) in enumerate(LARGE):
+    for i, (m, n, k) in enumerate(LARGE + FEW):
         a, b = gpu(integers(m, k, i)), gpu(integers(n, k, 50 + i))
         want = a.double() @ b.double().t()
         qa = mx.quantize(a) if raw is None else a.to(DT[raw])

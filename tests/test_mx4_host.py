@@ -170,8 +170,12 @@ def test_products_are_planned_within_their_limits(mx, shim):
             assert st == 0
             empty, quantize, shape, splits, per, a_scales, parts, ws = out
             lds = shim.shim_narrow_lds(ctypes.c_int64(m), ctypes.c_int64(k))
-            assert not empty and (shape == 0) == (m <= 64)
-            assert quantize == (raw and (m > 64 or lds > 48 * 1024))
+            assert not empty and (shape != 0 or m <= 64)
+            assert quantize == (raw and (shape != 0 or m * ref.widths(k)[0] * 2 > 24 * 1024))
+            if raw and not quantize:
+                assert lds <= 32 * 1024
+                units = -(-k // 128)  # rows of codes, 16 bytes apart, and their scales
+                assert lds >= m * (units * 64 + 16 + (units + 1) // 2 * 8)
             if quantize:
                 codes, scales = ref.widths(k)
                 assert a_scales % 256 == 0 and a_scales >= m * codes
