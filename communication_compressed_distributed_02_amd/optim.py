@@ -29,6 +29,7 @@ import torch
 
 from . import ob_adam as ob
 from . import ob_adamw as oa
+from . import ob_mx4 as mx
 
 
 def flat_layout(numels, n_workers):
@@ -161,12 +162,15 @@ class AdamWOptimizer(torch.optim.Optimizer):
     by the global gradient norm (0: no clipping), without a host wait; the last
     norm is in `norm` on the device.  skip_nonfinite: a step whose gradients are
     not all finite changes nothing.  A parameter without a gradient is left as it
-    is.  state_dict() / load_state_dict() carry the library's whole state and what it
+    is.  quantized: matrices among the parameters whose 4-bit copies (ob_mx4.Weight)
+    are kept in `quantized`, a dict by parameter, and written again by every step
+    that changes them: for ob_mx4.linear and ob_mx4.matmul.  Parameters that are
+    written otherwise need refresh().  state_dict() / load_state_dict() carry the library's whole state and what it
     was made with, all of which but grad_dtype has to be the same where it is loaded."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                  state_bits=32, master=False, stochastic=False, grad_dtype=None, max_norm=0.0,
-                 skip_nonfinite=False, seed=0, stream=None):
+                 skip_nonfinite=False, seed=0, stream=None, quantized=()):
         self._core = None
         super().__init__(params, dict(lr=lr, weight_decay=weight_decay))
         self.params = [p for g in self.param_groups for p in g["params"]]
@@ -175,6 +179,17 @@ class AdamWOptimizer(torch.optim.Optimizer):
         self._core = oa.AdamW([p.detach() for p in self.params], groups, len(self.param_groups),
                               grad_dtype, state_bits, master, stochastic, betas, eps, seed,
                               stream=stream)
+        quantized, own = tuple(quantized), {id(p) for p in self.params}
+        for p in quantized:
+            if id(p) not in own or p.dim() != 2:
+                raise ValueError("quantized are matrices among the parameters")
+        self.quantized = {p: mx.Weight(p) for p in quantized}
+
+    @torch.no_grad()
+    def refresh(self):
+        """Write the 4-bit copies again from the parameters as they are now."""
+        for p, w in self.quantized.items():
+            w.refresh(p)
 
     @property
     def core(self):
@@ -221,6 +236,9 @@ class AdamWOptimizer(torch.optim.Optimizer):
                                     self.max_norm, grad_scale, self.skip_nonfinite, sumsq)
         torch.autograd.graph.increment_version(
             [p for p, g in zip(self.params, grads) if g is not None])
+        for p, w in self.quantized.items():
+            if p.grad is not None:
+                w.refresh(p)
         return loss
 
     @property
