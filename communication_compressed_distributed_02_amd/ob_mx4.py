@@ -171,12 +171,28 @@ class MX4:
         q.scale_ptr = q.code_ptr + rows * c
         return q
 
+    @classmethod
+    def _pair(cls, x, rows, cols):
+        """Two for a matrix where the tensor x lies and its transpose, in one
+        allocation."""
+        a, b = object.__new__(cls), object.__new__(cls)
+        (ca, sa), (cb, sb) = _widths(cols), _widths(rows)
+        first = rows * (ca + sa)
+        held = x.new_empty(first + cols * (cb + sb), dtype=torch.uint8)
+        a.rows, a.cols, a.device, a._held = rows, cols, held.device, held
+        b.rows, b.cols, b.device, b._held = cols, rows, a.device, held
+        a.code_ptr = held.data_ptr()
+        a.scale_ptr = a.code_ptr + rows * ca
+        b.code_ptr = a.code_ptr + first
+        b.scale_ptr = b.code_ptr + cols * cb
+        return a, b
+
     def _part(self, i):
         if isinstance(self._held, tuple):
             return self._held[i]
-        width = _widths(self.cols)
-        begin = i * self.rows * width[0]
-        return self._held[begin:begin + self.rows * width[i]].view(self.rows, width[i])
+        width = _widths(self.cols)[i]
+        begin = (self.scale_ptr if i else self.code_ptr) - self._held.data_ptr()
+        return self._held[begin:begin + self.rows * width].view(self.rows, width)
 
     @property
     def codes(self):
@@ -291,9 +307,11 @@ def quantize_both(x, seed=None, out=None):
     flip = not _by_rows(m)
     if flip and m.stride(0) != 1 and m.shape[0] > 1:
         raise ValueError("x has strides %s: one dimension must be contiguous" % (m.stride(),))
-    rows, cols = (None, None) if out is None else out
-    rows = _target(rows, m.shape[0], m.shape[1], x, "the first of out")
-    cols = _target(cols, m.shape[1], m.shape[0], x, "the second of out")
+    if out is None:
+        rows, cols = MX4._pair(x, m.shape[0], m.shape[1])
+    else:
+        rows = _target(out[0], m.shape[0], m.shape[1], x, "the first of out")
+        cols = _target(out[1], m.shape[1], m.shape[0], x, "the second of out")
     if flip:
         _quantize(m.t(), seed, None, cols, rows)
     else:
@@ -369,17 +387,24 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     c = _result(out, rows, b.rows, dtype, device)
-    args = ob_mx4_matmul_args(rows, b.rows, cols, *given, _TYPES[dtype], stride, b.code_ptr,
-                              b.scale_ptr, c.data_ptr(), _row_stride(c), bool(accumulate), None, 0)
-    need = _workspace(args, rows, b.rows, cols, args.a_codes is None)
-    if need:
-        # freed to torch's allocator on return: later work of this stream may have it then
-        scratch = torch.empty(need, dtype=torch.uint8, device=device)
-        args.workspace, args.ws_bytes = scratch.data_ptr(), need
-    _on(device, ob_mx4_matmul, args)
+    _product(given, stride, rows, cols, b, c, dtype, accumulate)
     if shape is not None and len(shape) != 1 and out is None:
         return c.view(*shape, b.rows)
     return c
+
+
+def _product(given, stride, rows, cols, b, c, dtype, accumulate=False):
+    """c = a b^T, or added to it; given: a's codes, scales, plain elements and
+    their type."""
+    args = ob_mx4_matmul_args(rows, b.rows, cols, *given, _TYPES[dtype], stride, b.code_ptr,
+                              b.scale_ptr, c.data_ptr(), c.stride(0) if rows > 1 else b.rows,
+                              accumulate, None, 0)
+    need = _workspace(args, rows, b.rows, cols, given[0] is None)
+    if need:
+        # freed to torch's allocator on return: later work of this stream may have it then
+        scratch = c.new_empty(need, dtype=torch.uint8)
+        args.workspace, args.ws_bytes = scratch.data_ptr(), need
+    _on(b.device, ob_mx4_matmul, args)
 
 
 class Weight:
@@ -400,8 +425,15 @@ class Weight:
 
 def _unit(x):
     """x as a matrix that quantize_both takes (a copy where it has to be)."""
-    m = x.reshape(-1, x.shape[-1]) if x.dim() != 2 else x
+    m = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
     return m if _by_rows(m) or m.stride(0) == 1 else m.contiguous()
+
+
+def _of_mx4(a, b, like, dtype, shape=None):
+    """a b^T of two MX4 that fit, as a new tensor where `like` lies."""
+    c = like.new_empty((a.rows, b.rows), dtype=dtype)
+    _product((a.code_ptr, a.scale_ptr, None, 0), 0, a.rows, a.cols, b, c, dtype)
+    return c if shape is None or len(shape) == 2 else c.view(shape)
 
 
 class _Linear(torch.autograd.Function):
@@ -409,22 +441,22 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, quantized, seed):
         need_x, need_w = ctx.needs_input_grad[:2]
         m = _unit(x)
-        if quantized is None:
-            if need_x:
-                w, ctx.w_cols = quantize_both(weight)
-            else:
-                w = quantize(weight)
-        else:
-            w, ctx.version = quantized.rows, quantized.version
-            if need_x:
-                ctx.w_cols = quantized.cols
         ctx.quantized = quantized
+        if quantized is not None:
+            w, ctx.w_cols, ctx.version = quantized.rows, quantized.cols, quantized.version
+        elif need_x:
+            w, ctx.w_cols = quantize_both(weight)
+        else:
+            w = quantize(weight)
+        ctx.seed, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = seed, x.shape, x.dtype, weight.dtype
+        shape = (*x.shape[:-1], weight.shape[0])
         if need_w:
             a, ctx.x_cols = quantize_both(m)
+        elif _by_rows(m):
+            return matmul(m, w, x.dtype).view(shape)
         else:
-            a = m if _by_rows(m) else quantize(m)
-        ctx.seed, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = seed, x.shape, x.dtype, weight.dtype
-        return matmul(a, w, x.dtype).view(*x.shape[:-1], weight.shape[0])
+            a = quantize(m)
+        return _of_mx4(a, w, m, x.dtype, shape)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -441,9 +473,9 @@ class _Linear(torch.autograd.Function):
         elif need_w:
             g_cols = quantize(dy.t(), ctx.seed)
         if need_x:
-            dx = matmul(g, ctx.w_cols, ctx.x_dtype).view(ctx.x_shape)
+            dx = _of_mx4(g, ctx.w_cols, dy, ctx.x_dtype, ctx.x_shape)
         if need_w:
-            dw = matmul(g_cols, ctx.x_cols, ctx.w_dtype)
+            dw = _of_mx4(g_cols, ctx.x_cols, dy, ctx.w_dtype)
         return dx, dw, None, None
 
 
