@@ -83,6 +83,14 @@ __device__ __forceinline__ void store1(bf16* p, float c) {
   p->bits = (uint16_t)pack_bf16(c, c);
 }
 
+// Blocks go to the 8 dies in turn: the block's place in an order that gives each
+// die a run of neighbours, which then share its cache.
+__device__ __forceinline__ uint32_t on_one_die(uint32_t block, uint32_t all) {
+  constexpr uint32_t kDies = 8;
+  const uint32_t per = all / kDies, more = all % kDies, die = block % kDies;
+  return die * per + (die < more ? die : more) + block / kDies;
+}
+
 // What this wave wrote to LDS is there for all its lanes.
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");

@@ -125,11 +125,18 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
 }
 
 // The transposed matrix, and the rows too where codes is not null, from one
-// read: a wave holds 32 rows of 256 columns in registers, 4 columns a lane, so
-// that a block down a column lies on one lane and one along a row on 8.  The
-// transposed codes of 4 waves go through LDS to be written as 64 bytes of a
-// column, the scales of both as words.
-constexpr int kTileCols = 256, kTileWaves = 4, kTileRows = kTileWaves * kBlockElems;
+// read: a wave holds 32 rows of 128 columns in registers, 16 rows of 4 columns a
+// lane (the upper lanes the lower rows), so that a block down a column lies on
+// two lanes and one along a row on 8.  The transposed codes of 4 waves go through
+// LDS to be written as 64 bytes of a column, the scales of both as words.
+// 16384 x 6400 bfloat16 elements in 75 us (4.3 TB/s; with the tile itself in
+// LDS 131), 4096 x 1024 in 6.4.  Stochastically 100 us: 23 instructions an element for
+// two results, half of them the hash.  32 rows of 256 columns a wave: 79 and
+// 104 us, 4096 x 1024 8.0, where they are too few.  Neighbours on one die merge
+// their halves of lines: 75 against 78 without (fp32, whose lines are whole, 131
+// against 120 at this size, 23 against 25 at a quarter of it).
+constexpr int kTileCols = 128, kTileWaves = 4, kTileRows = kTileWaves * kBlockElems;
+constexpr int kLaneRows = 16;
 template <typename T>
 struct Four;  // 4 neighbouring elements
 template <>
@@ -177,11 +184,11 @@ struct Four<bf16> {
   }
 };
 
-// Column j of 32 rows: its largest magnitude, and 8 of its codes at a time.
+// Column j of a lane's 16 rows: its largest magnitude, and 8 of its codes at a time.
 __device__ __forceinline__ uint32_t column_top(const Four<float>* x, int j) {
   uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < kBlockElems; ++i) {
+  for (int i = 0; i < kLaneRows; ++i) {
     const uint32_t w = magnitude(x[i].w[j]);
     top = w > top ? w : top;
   }
@@ -190,7 +197,7 @@ __device__ __forceinline__ uint32_t column_top(const Four<float>* x, int j) {
 __device__ __forceinline__ uint32_t column_top(const Four<bf16>* x, int j) {
   u16x2 top = magnitudes(x[0].w[j >> 1]);  // of two columns, once for both
 #pragma unroll
-  for (int i = 1; i < kBlockElems; ++i)
+  for (int i = 1; i < kLaneRows; ++i)
     top = __builtin_elementwise_max(top, magnitudes(x[i].w[j >> 1]));
   return (uint32_t)top[j & 1] << 16;
 }
@@ -215,48 +222,53 @@ __device__ __forceinline__ uint32_t column_codes(const Four<bf16>* x, int j, uin
 
 template <typename T, bool STOCHASTIC, bool WIDE>
 __global__ void __launch_bounds__(kTileWaves * 64) quantize_tiles_kernel(QuantizeArgs a) {
-  __shared__ __attribute__((aligned(16))) u32x4 out[kTileCols * kTileWaves];
-  __shared__ __attribute__((aligned(8))) uint8_t out_scale[kTileCols * kTileWaves];
-  __shared__ __attribute__((aligned(8))) uint8_t row_scale[kTileRows * 8];
+  constexpr int kPieces = kTileRows / kLaneRows;  // 8 bytes each of a column's codes
+  __shared__ __attribute__((aligned(16))) u32x2 out[kTileCols * kPieces];
+  __shared__ __attribute__((aligned(4))) uint8_t out_scale[kTileCols * kTileWaves];
+  __shared__ __attribute__((aligned(4))) uint8_t row_scale[kTileRows * (kTileCols / kBlockElems)];
   const int64_t tiles_c = (a.cols + kTileCols - 1) / kTileCols;
-  const int64_t tr = (int64_t)blockIdx.x / tiles_c, tc = (int64_t)blockIdx.x - tr * tiles_c;
+  const uint32_t tile = on_one_die(blockIdx.x, gridDim.x);
+  const int64_t tr = (int64_t)tile / tiles_c, tc = (int64_t)tile - tr * tiles_c;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int lane = (int)threadIdx.x & 63;
-  const int64_t r0 = tr * kTileRows + wave * kBlockElems, c0 = tc * kTileCols, col = c0 + lane * 4;
+  const int lane = (int)threadIdx.x & 31, half = (int)threadIdx.x >> 5 & 1;
+  const int64_t first_row = tr * kTileRows, c0 = tc * kTileCols, col = c0 + lane * 4;
+  const int lr0 = wave * kBlockElems + half * kLaneRows;  // in the tile
+  const int64_t r0 = first_row + lr0;
   const int64_t rc = row_codes(a.cols), rs = row_scales(a.cols);
   Keys keys{};
   if (STOCHASTIC) keys = call_keys(a);
-  Four<T> x[kBlockElems];
-  const int rows = (int)(a.rows - r0 < kBlockElems ? a.rows - r0 : kBlockElems);
-  const int64_t first_row = tr * kTileRows;
-  if (rows == kBlockElems && c0 + kTileCols <= a.cols) {
+  Four<T> x[kLaneRows];
+  const T* from = (const T*)a.x + r0 * a.stride + col;
+  if (first_row + kTileRows <= a.rows && c0 + kTileCols <= a.cols) {
 #pragma unroll
-    for (int i = 0; i < kBlockElems; ++i) x[i].load((const T*)a.x + (r0 + i) * a.stride + col);
+    for (int i = 0; i < kLaneRows; ++i) x[i].load(from + i * a.stride);
   } else {
     // at an edge: zeros where there are no elements
 #pragma unroll
-    for (int i = 0; i < kBlockElems; ++i) x[i].clear();
+    for (int i = 0; i < kLaneRows; ++i) x[i].clear();
     if (col + 4 <= a.cols) {
 #pragma unroll
-      for (int i = 0; i < kBlockElems; ++i)
-        if (i < rows) x[i].load((const T*)a.x + (r0 + i) * a.stride + col);
+      for (int i = 0; i < kLaneRows; ++i)
+        if (r0 + i < a.rows) x[i].load(from + i * a.stride);
     } else if (col < a.cols) {
 #pragma unroll
-      for (int i = 0; i < kBlockElems; ++i)
-        if (i < rows)
-          x[i].load_some((const T*)a.x + (r0 + i) * a.stride + col, (int)(a.cols - col));
+      for (int i = 0; i < kLaneRows; ++i)
+        if (r0 + i < a.rows) x[i].load_some(from + i * a.stride, (int)(a.cols - col));
     }
   }
   if (a.codes != nullptr) {
-    const bool inside = col < padded(a.cols);
+    uint8_t* to = a.codes + r0 * rc + col / 2;
+    const uint64_t quad = (uint64_t)(r0 * (padded(a.cols) / 4) + col / 4);
 #pragma unroll
-    for (int i = 0; i < kBlockElems; ++i) {
+    for (int i = 0; i < kLaneRows; ++i) {
       const uint32_t byte = scale_byte<STOCHASTIC>(oct_max(x[i].top()));
-      const uint64_t quad = (uint64_t)((r0 + i) * (padded(a.cols) / 4) + col / 4);
-      const uint32_t codes = STOCHASTIC ? x[i].template stochastic<WIDE>(byte, quad, keys)
-                                        : x[i].encode(byte);
-      if (i < rows && inside) *(uint16_t*)(a.codes + (r0 + i) * rc + col / 2) = (uint16_t)codes;
-      if ((lane & 7) == 0) row_scale[(wave * kBlockElems + i) * 8 + lane / 8] = (uint8_t)byte;
+      const uint32_t codes =
+          STOCHASTIC ? x[i].template stochastic<WIDE>(
+                           byte, quad + (uint64_t)i * (uint64_t)(padded(a.cols) / 4), keys)
+                     : x[i].encode(byte);
+      // the columns of a tile are those of the padding
+      if (r0 + i < a.rows) *(uint16_t*)(to + i * rc) = (uint16_t)codes;
+      if ((lane & 7) == 0) row_scale[(lr0 + i) * 4 + lane / 8] = (uint8_t)byte;
       // few rows at a time, so that the registers do
       if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);
     }
@@ -264,53 +276,50 @@ __global__ void __launch_bounds__(kTileWaves * 64) quantize_tiles_kernel(Quantiz
   // The values are taken apart again from here on: kept from the rows they would
   // take twice the registers.
 #pragma unroll
-  for (int i = 0; i < kBlockElems; ++i) asm volatile("" : "+v"(x[i].w));
+  for (int i = 0; i < kLaneRows; ++i) asm volatile("" : "+v"(x[i].w));
   const int64_t trc = row_codes(a.rows), trs = row_scales(a.rows);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t byte = scale_byte<STOCHASTIC>(column_top(x, j));
+    const uint32_t top = column_top(x, j);
+    const u32x2 both =
+        __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(top, top, false, false));
+    const uint32_t byte = scale_byte<STOCHASTIC>(both.x > both.y ? both.x : both.y);
     const uint64_t quad = (uint64_t)((col + j) * (padded(a.rows) / 4) + r0 / 4);
-    u32x4 codes;
+    u32x2 codes;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 2; ++k)
       codes[k] = column_codes<STOCHASTIC, WIDE>(x + 8 * k, j, byte, quad + 2 * k, keys);
-    // lanes that write together are 4 columns apart: each to a place of its own
-    out[(lane * 4 + j) * kTileWaves + (wave ^ (lane & (kTileWaves - 1)))] = codes;
-    out_scale[(lane * 4 + j) * kTileWaves + wave] = (uint8_t)byte;
+    // lanes that write together are 4 columns apart: their pieces are permuted
+    out[(lane * 4 + j) * kPieces + ((wave ^ (lane & 3)) * 2 + half)] = codes;
+    if (half == 0) out_scale[(lane * 4 + j) * kTileWaves + wave] = (uint8_t)byte;
     __builtin_amdgcn_sched_barrier(0);
   }
   __syncthreads();
 #pragma unroll
   for (int t = 0; t < kTileCols / 64; ++t) {
-    const int i = t * kTileWaves * 64 + (int)threadIdx.x, lc = i / kTileWaves, piece = i % kTileWaves;
-    const int64_t at = first_row / 2 + piece * 16;
-    if (c0 + lc < a.cols && at < trc)
-      *(u32x4*)(a.codes_t + (c0 + lc) * trc + at) =
-          out[lc * kTileWaves + (piece ^ (lc / 4 & (kTileWaves - 1)))];
+    const int i = t * kTileWaves * 64 + (int)threadIdx.x, lc = i / 4, piece = i % 4;
+    if (c0 + lc < a.cols)
+      *(u32x4*)(a.codes_t + (c0 + lc) * trc + first_row / 2 + piece * 16) =
+          *(const u32x4*)&out[lc * kPieces + (piece ^ (lc / 4 & 3)) * 2];
   }
-  // scales in words of 4; those of rows that do not exist are zero, and the last
-  // tile's go on to the end of the padding
-  const int64_t tiles_r = (a.rows + kTileRows - 1) / kTileRows;
-  for (int i = (int)threadIdx.x; i < kTileCols * kTileWaves / 4; i += kTileWaves * 64) {
-    const int lc = i / (kTileWaves / 4), part = i % (kTileWaves / 4);
-    const int64_t at = first_row / kBlockElems + part * 4;
-    if (c0 + lc >= a.cols) continue;
-    uint8_t* to = a.scales_t + (c0 + lc) * trs;
-    if (at < trs) *(uint32_t*)(to + at) = *(const uint32_t*)&out_scale[lc * kTileWaves + part * 4];
-    if (part == 0 && tr == tiles_r - 1)
-      for (int64_t k = tiles_r * kTileWaves; k < trs; k += 4) *(uint32_t*)(to + k) = 0;
-  }
-  if (a.codes != nullptr) {
-    for (int i = (int)threadIdx.x; i < kTileRows * 2; i += kTileWaves * 64) {
-      const int64_t row = first_row + i / 2, at = c0 / kBlockElems + (i & 1) * 4;
-      if (row >= a.rows) continue;
-      uint8_t* to = a.scales + row * rs;
-      if (at < rs) *(uint32_t*)(to + at) = *(const uint32_t*)&row_scale[i * 4];
-      if ((i & 1) == 0 && tc == tiles_c - 1)
-        for (int64_t k = tiles_c * 8; k < rs; k += 4) *(uint32_t*)(to + k) = 0;
+  // a word of scales for a column, one for a row; the last tile's go on to the
+  // end of the padding
+  const int i = (int)threadIdx.x & 127;
+  if (threadIdx.x < 128) {
+    if (c0 + i < a.cols) {
+      uint32_t* to = (uint32_t*)(a.scales_t + (c0 + i) * trs);
+      to[tr] = *(const uint32_t*)&out_scale[i * 4];
+      if (first_row + kTileRows >= a.rows)
+        for (int64_t k = tr + 1; k < trs / 4; ++k) to[k] = 0;
     }
+  } else if (a.codes != nullptr && first_row + i < a.rows) {
+    uint32_t* to = (uint32_t*)(a.scales + (first_row + i) * rs);
+    to[tc] = *(const uint32_t*)&row_scale[i * 4];
+    if (tc == tiles_c - 1)
+      for (int64_t k = tc + 1; k < rs / 4; ++k) to[k] = 0;
   }
 }
+static_assert(kTileRows == 128 && kTileCols == 128, "a thread for each row and column's scales");
 
 // Mean of n messages, 8 elements a lane; the loads of kAhead messages at a time: 8
 // messages of 110M elements in 165-176 us (5.2-5.5 TB/s; one message after the

@@ -244,18 +244,15 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
          (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(x >> 32)) << 32;
 }
 
-// Tiles in an order that keeps neighbours on one die: blocks go to the 8 dies
-// in turn, each die gets a run of tiles, and a run goes down kGroup tiles of a
-// before it moves along b.  6 and not a power of two, with which the tiles that
+// Tiles in an order that keeps neighbours on one die: a die's run goes down kGroup
+// tiles of a before it moves along b.  6 and not a power of two, with which the tiles that
 // run together meet in the same memory channels: out of memory that is not in
 // the caches, 16384 x 6400 x 1600 125 us (8: 148, 4: 134, 7: 123, 12: 131), 8192
 // x 8192 x 1024 56 (8 and 4: 67), 16384 x 1600 x 6400 102 (8: 112, 4: 98, 7: 112).
-constexpr int kDies = 8, kGroup = 6;
+constexpr int kGroup = 6;
 __device__ __forceinline__ void tile_of(uint32_t block, uint32_t tiles_m, uint32_t tiles_n,
                                         uint32_t* tm, uint32_t* tn) {
-  const uint32_t all = tiles_m * tiles_n, per = all / kDies, more = all % kDies;
-  const uint32_t die = block % kDies, at = block / kDies;
-  const uint32_t t = die * per + (die < more ? die : more) + at;
+  const uint32_t t = on_one_die(block, tiles_m * tiles_n);
   const uint32_t in_group = kGroup * tiles_n, g = t / in_group, r = t - g * in_group;
   const uint32_t high = tiles_m - g * kGroup < kGroup ? tiles_m - g * kGroup : kGroup;
   *tn = r / high;
