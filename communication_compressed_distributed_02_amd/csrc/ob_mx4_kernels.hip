@@ -386,8 +386,6 @@ __global__ void __launch_bounds__(kThreads) average_kernel(AverageArgs a) {
 int64_t blocks_for(int64_t rows, int64_t cols, int64_t per) {
   return (rows * (padded(cols) / kLaneElems) + per - 1) / per;
 }
-// A grid's first dimension holds 2^31 - 1 blocks: 2^40 elements in blocks of 2048
-// and more stay below it.
 constexpr int kUnroll = 2;
 
 // Whether the index of four elements of rows x cols, padded, may pass 2^32.

@@ -14,9 +14,10 @@ constexpr int kBlockElems = 32;   // elements of one scale
 constexpr int kPadElems = 128;    // a row of codes is padded to so many elements
 constexpr int kScalePad = 16;     // and a row of scales to so many bytes
 constexpr int kMaxMessages = OB_MX4_MAX_MESSAGES;
-constexpr int64_t kMaxElems = int64_t(1) << 40;  // of padded rows; no size below can overflow
+// Elements in padded rows: a launch counts at most 2^32 threads, and the kernels
+// that take fewest, 4096 a block of 256, stay below half of that.
+constexpr int64_t kMaxElems = int64_t(1) << 35;
 constexpr int64_t kMaxK = int64_t(1) << 24;      // 255 rows of k / 2 bytes stay below 2^32
-constexpr int64_t kMaxDim = int64_t(1) << 30;    // rows and columns of a product
 
 constexpr int64_t up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
 constexpr int64_t padded(int64_t cols) { return up(cols, kPadElems); }
@@ -31,7 +32,7 @@ inline bool flag(int32_t v) { return v == 0 || v == 1; }
 // Rows and columns that a quantised matrix may have, in that order.
 inline bool shape(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > kMaxElems || cols > kMaxElems) return false;
-  return rows == 0 || row_scales(cols) * kBlockElems <= kMaxElems / rows;
+  return rows == 0 || padded(cols) <= kMaxElems / rows;
 }
 
 // A stride that keeps every offset of rows x cols elements below 2^60.
@@ -118,6 +119,7 @@ struct Product {
 };
 
 constexpr int kNarrowRows = 64;        // rows of a that the narrow kernel takes at most
+constexpr int64_t kNarrowCols = int64_t(1) << 26;  // 16 a block of 512 threads
 constexpr int kNarrowLds = 32 * 1024;  // bytes of LDS that it uses at most
 // Elements of an a that it quantises itself, by every block: 16 rows of 1024
 // 4.4 us, 2.0 and 3.1 in two launches; 16 of 1600 8.2, and 2.0 and 4.4.
@@ -172,14 +174,13 @@ inline ob_status plan_product(const ob_mx4_matmul_args* a, Product* out) {
   const bool packed = a->a_codes != nullptr || a->a_scales != nullptr;
   if (!packed && !dtype(a->a_dtype)) return OB_ERR_ARG;
   const int64_t m = a->m, n = a->n, k = a->k;
-  if (m < 0 || n < 0 || k < 0 || m > kMaxDim || n > kMaxDim || k > kMaxK || !shape(m, k) ||
-      !shape(n, k) || !shape(m, n))
+  if (k < 0 || k > kMaxK || !shape(m, k) || !shape(n, k) || !shape(m, n) || !shape(n, m))
     return OB_ERR_SHAPE;
   *out = Product{};
   out->empty = m == 0 || n == 0;
   if (out->empty || k == 0) return OB_OK;
   const double time = choose_tiles(m, n, k, out);
-  if (m <= kNarrowRows && narrow_time(m, n, k) <= time) {
+  if (m <= kNarrowRows && n <= kNarrowCols && narrow_time(m, n, k) <= time) {
     out->shape = kNarrow;
     out->splits = out->per_split = 0;
   }

@@ -510,8 +510,8 @@ hipError_t tiles(const ProductArgs& p, Shape shape, int splits, int per_split, h
 
 template <typename T>
 __global__ void __launch_bounds__(256) empty_kernel(ProductArgs p) {
-  for (int u = 0; u < 4; ++u) {
-    const int64_t i = ((int64_t)blockIdx.x * 4 + u) * 256 + threadIdx.x;
+  for (int u = 0; u < 16; ++u) {
+    const int64_t i = ((int64_t)blockIdx.x * 16 + u) * 256 + threadIdx.x;
     const int64_t row = i / p.n;
     if (row < p.m) store1((T*)p.out + row * p.out_stride + (i - row * p.n), 0.0f);
   }
@@ -567,7 +567,7 @@ hipError_t launch_product_tiles(const ProductArgs& p, Shape shape, int splits, i
 
 hipError_t launch_product_empty(const ProductArgs& p, bool out_bf16, hipStream_t stream) {
   if (p.accumulate) return hipSuccess;
-  const dim3 grid((uint32_t)((p.m * p.n + 1023) / 1024));
+  const dim3 grid((uint32_t)((p.m * p.n + 4095) / 4096));
   if (out_bf16)
     empty_kernel<bf16><<<grid, 256, 0, stream>>>(p);
   else

@@ -16,6 +16,7 @@ not fit and ObAdamError on a status other than OB_OK.  Every computation runs
 in the library's HIP kernels; there is no fallback.
 """
 import ctypes
+import math
 
 import torch
 
@@ -171,22 +172,6 @@ class MX4:
         q.scale_ptr = q.code_ptr + rows * c
         return q
 
-    @classmethod
-    def _pair(cls, x, rows, cols):
-        """Two for a matrix where the tensor x lies and its transpose, in one
-        allocation."""
-        a, b = object.__new__(cls), object.__new__(cls)
-        (ca, sa), (cb, sb) = _widths(cols), _widths(rows)
-        first = rows * (ca + sa)
-        held = x.new_empty(first + cols * (cb + sb), dtype=torch.uint8)
-        a.rows, a.cols, a.device, a._held = rows, cols, held.device, held
-        b.rows, b.cols, b.device, b._held = cols, rows, a.device, held
-        a.code_ptr = held.data_ptr()
-        a.scale_ptr = a.code_ptr + rows * ca
-        b.code_ptr = a.code_ptr + first
-        b.scale_ptr = b.code_ptr + cols * cb
-        return a, b
-
     def _part(self, i):
         if isinstance(self._held, tuple):
             return self._held[i]
@@ -227,11 +212,8 @@ def _matrix(x, what):
         return x
     if x.dim() == 0:
         raise ValueError("%s must have a dimension" % what)
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
     try:
-        return x.view(rows, x.shape[-1])
+        return x.view(math.prod(x.shape[:-1]), x.shape[-1])
     except RuntimeError:
         raise ValueError("%s of shape %s and strides %s is no matrix: make it contiguous"
                          % (what, tuple(x.shape), x.stride())) from None
@@ -307,11 +289,9 @@ def quantize_both(x, seed=None, out=None):
     flip = not _by_rows(m)
     if flip and m.stride(0) != 1 and m.shape[0] > 1:
         raise ValueError("x has strides %s: one dimension must be contiguous" % (m.stride(),))
-    if out is None:
-        rows, cols = MX4._pair(x, m.shape[0], m.shape[1])
-    else:
-        rows = _target(out[0], m.shape[0], m.shape[1], x, "the first of out")
-        cols = _target(out[1], m.shape[1], m.shape[0], x, "the second of out")
+    rows, cols = (None, None) if out is None else out
+    rows = _target(rows, m.shape[0], m.shape[1], x, "the first of out")
+    cols = _target(cols, m.shape[1], m.shape[0], x, "the second of out")
     if flip:
         _quantize(m.t(), seed, None, cols, rows)
     else:
@@ -425,7 +405,7 @@ class Weight:
 
 def _unit(x):
     """x as a matrix that quantize_both takes (a copy where it has to be)."""
-    m = x if x.dim() == 2 else x.reshape(-1, x.shape[-1])
+    m = x if x.dim() == 2 else x.reshape(math.prod(x.shape[:-1]), x.shape[-1])
     return m if _by_rows(m) or m.stride(0) == 1 else m.contiguous()
 
 
@@ -496,6 +476,8 @@ def linear(x, weight, quantized=None, seed=None):
         if t.dtype not in _TYPES:
             raise ValueError("%s must be float32 or bfloat16, not %s" % (what, t.dtype))
         _need_gpu(t, what)
-    if quantized is not None and quantized.rows.shape != tuple(weight.shape):
-        raise ValueError("quantized is of a weight of %d x %d" % quantized.rows.shape)
+    if quantized is not None and (quantized.rows.shape != tuple(weight.shape)
+                                  or quantized.rows.device != weight.device):
+        raise ValueError("quantized is of a weight of %d x %d on %s"
+                         % (*quantized.rows.shape, quantized.rows.device))
     return _Linear.apply(x, weight, quantized, seed)

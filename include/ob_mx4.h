@@ -43,7 +43,9 @@
  * with memory of their own may run on several streams at once.  Argument errors
  * return before anything is enqueued; a HIP error returns OB_ERR_HIP.  Memory
  * that is written may not overlap what else the call reads or writes
- * (OB_ERR_ARG), except where stated.  No C++ exception crosses this interface.
+ * (OB_ERR_ARG), except where stated; memory is taken from its first element to its
+ * last, what lies between strided rows included.  No C++ exception crosses this
+ * interface.
  */
 #ifndef OB_MX4_H
 #define OB_MX4_H
@@ -60,7 +62,8 @@ enum { OB_MX4_F32 = OB_GRAD_F32, OB_MX4_BF16 = OB_GRAD_BF16 };
 enum { OB_MX4_MAX_MESSAGES = 64 };
 
 /* Bytes of a row of codes and of scales.  rows and cols may be 0; OB_ERR_SHAPE
- * for a negative one, and for more than 2^40 elements in padded rows. */
+ * for a negative one, and for more than 2^35 elements in padded rows, here and
+ * for every matrix of the calls below. */
 ob_status ob_mx4_layout(int64_t rows, int64_t cols, int64_t* row_codes, int64_t* row_scales);
 
 typedef struct {
@@ -81,8 +84,8 @@ typedef struct {
 
 ob_status ob_mx4_quantize(const ob_mx4_quantize_args* args, void* stream);
 
-/* Mean of n messages (1 .. OB_MX4_MAX_MESSAGES; 1 reads a matrix back) of rows x
- * cols.  codes, scales: host arrays of n device pointers, 16-byte aligned; they
+/* Mean of n messages (1 .. OB_MX4_MAX_MESSAGES, OB_ERR_SHAPE otherwise; 1 reads a
+ * matrix back) of rows x cols.  codes, scales: host arrays of n device pointers, 16-byte aligned; they
  * may repeat.  Element (r, c) goes to out[r * stride + c], stride >= cols, of
  * type dtype. */
 ob_status ob_mx4_average(const void* const* codes, const void* const* scales, int32_t n,
@@ -90,7 +93,8 @@ ob_status ob_mx4_average(const void* const* codes, const void* const* scales, in
                          void* stream);
 
 typedef struct {
-  int64_t m, n, k;      /* out is m x n, a m x k, b n x k; k <= 2^24 */
+  int64_t m, n, k;      /* out is m x n (and n x m as large as a matrix may be), a m x k, b
+                           n x k; k <= 2^24 */
   const void* a_codes;  /* 16-byte aligned; NULL with a_scales: a is given in a */
   const void* a_scales;
   const void* a;        /* element (i, k) at a[i * a_stride + k]: quantised to nearest on the way */

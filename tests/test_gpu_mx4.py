@@ -433,9 +433,15 @@ def test_linear_shapes_and_partial_gradients(mx):
     assert torch.equal(mx.linear(x.detach()[0, 0, 0], w), x.detach()[0, 0, 0] @ w.t())
     v = gpu(integers(36, 8, 3))
     assert torch.equal(mx.linear(v.t(), w), v.t() @ w.t())
-    e = torch.empty(0, 36, device="cuda", requires_grad=True)
-    mx.linear(e, w).sum().backward()
-    assert e.grad.shape == (0, 36)
+    for shape in ((0, 36), (2, 0, 36)):
+        e = torch.empty(shape, device="cuda", requires_grad=True)
+        mx.linear(e, w).sum().backward()
+        assert e.grad.shape == shape
+    none = torch.empty(24, 0, device="cuda", requires_grad=True)
+    y = mx.linear(torch.empty(2, 3, 0, device="cuda", requires_grad=True), none)
+    assert y.shape == (2, 3, 24) and (y == 0).all()
+    y.sum().backward()
+    assert none.grad.shape == (24, 0)
     # copies refreshed in between are told
     kept = mx.Weight(w)
     y = mx.linear(x, w, kept)

@@ -33,10 +33,10 @@ def test_library_exports_every_declared_symbol(mx):
 
 
 def test_layout(mx):
-    for rows, cols in ((0, 0), (1, 0), (3, 1), (1, 128), (2, 129), (5, 512), (5, 513), (1, 1 << 33)):
+    for rows, cols in ((0, 0), (1, 0), (3, 1), (1, 128), (2, 129), (5, 512), (5, 513), (1, 1 << 33),
+                       (1 << 28, 3), (1, 1 << 35)):
         assert mx.ob_mx4_layout(rows, cols) == ref.widths(cols)
-    assert mx.ob_mx4_layout(1, 1 << 40) == ref.widths(1 << 40)
-    for rows, cols in ((-1, 1), (1, -1), (1, (1 << 40) + 1), ((1 << 31) + 1, 1), (1 << 20, (1 << 20) + 1),
+    for rows, cols in ((-1, 1), (1, -1), (1, (1 << 35) + 1), ((1 << 28) + 1, 1), (1 << 20, (1 << 15) + 1),
                        ((1 << 63) - 1, (1 << 63) - 1)):
         refused(mx, lambda: mx.ob_mx4_layout(rows, cols), "SHAPE")
 
@@ -76,8 +76,8 @@ def test_quantize_refusals(mx):
                dict(residual=place(1) - 4 * 799), dict(both, codes_t=place(1) + 8 * 64 - 16),
                dict(both, scales_t=place(2)), dict(seed_device=place(1) + 8)):
         refused(mx, lambda: mx.ob_mx4_quantize(quantize_args(mx, **kw), None), "ARG")
-    for kw in (dict(rows=-1), dict(cols=-1), dict(rows=1 << 32, cols=1), dict(cols=1 << 41),
-               dict(both, rows=1, cols=1 << 32)):
+    for kw in (dict(rows=-1), dict(cols=-1), dict(rows=(1 << 28) + 1, cols=1), dict(cols=1 << 33),
+               dict(both, rows=1, cols=(1 << 28) + 1)):
         refused(mx, lambda: mx.ob_mx4_quantize(quantize_args(mx, **kw), None), "SHAPE")
     with pytest.raises(ctypes.ArgumentError):
         mx._lib.ob_mx4_quantize(1, None)
@@ -97,7 +97,7 @@ def test_average_refusals(mx):
                dict(scales=(place(2) + 8, place(3))), dict(codes=(place(0), place(1) + 1)),
                dict(out=place(1)), dict(out=place(3) + 8 * 16 - 4), dict(out=place(0) - 4 * 799)):
         refused(mx, lambda: call(**kw), "ARG")
-    for kw in (dict(rows=-1), dict(cols=1 << 41, stride=1 << 41), dict(codes=(), scales=()),
+    for kw in (dict(rows=-1), dict(cols=1 << 36, stride=1 << 36), dict(codes=(), scales=()),
                dict(codes=(place(0),) * 65, scales=(place(2),) * 65)):
         refused(mx, lambda: call(**kw), "SHAPE")
     call(rows=0, out=None)
@@ -124,8 +124,8 @@ def test_matmul_refusals(mx):
                dict(b_scales=place(3) + 8), dict(out=place(0)), dict(out=place(3) + 796),
                dict(raw, out=place(5))):
         refused(mx, lambda: mx.ob_mx4_matmul(matmul_args(mx, **kw), None), "ARG")
-    for kw in (dict(m=-1), dict(n=-1), dict(k=-1), dict(k=(1 << 24) + 1), dict(m=(1 << 30) + 1),
-               dict(n=(1 << 30) + 1), dict(m=1 << 30, n=1 << 30, out_stride=1 << 30)):
+    for kw in (dict(m=-1), dict(n=-1), dict(k=-1), dict(k=(1 << 24) + 1), dict(m=(1 << 28) + 1),
+               dict(n=(1 << 28) + 1), dict(m=1 << 20, n=1 << 20, out_stride=1 << 20)):
         refused(mx, lambda: mx.ob_mx4_matmul(matmul_args(mx, **kw), None), "SHAPE")
         refused(mx, lambda: mx.ob_mx4_matmul_workspace(matmul_args(mx, **kw)), "SHAPE")
     for kw in (dict(m=0), dict(n=0, out_stride=0)):
@@ -155,7 +155,7 @@ def test_products_are_planned_within_their_limits(mx, shim):
     r = np.random.default_rng(1)
     sizes = [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1000, 1600, 4096,
              6400, 16384, 1 << 20, 1 << 24]
-    cases = [tuple(r.choice(sizes, 3)) for _ in range(3000)] + [(1 << 30, 1, 1), (1, 1 << 30, 1),
+    cases = [tuple(r.choice(sizes, 3)) for _ in range(3000)] + [(1 << 28, 1, 1), (1, 1 << 28, 1),
                                                                (1, 1, 1 << 24), (64, 64, 1 << 24)]
     for m, n, k in cases:
         m, n, k = int(m), int(n), int(k)
@@ -164,7 +164,8 @@ def test_products_are_planned_within_their_limits(mx, shim):
             a = matmul_args(mx, m=m, n=n, k=k, out_stride=n, **kw)
             out = (ctypes.c_int64 * 8)()
             st = shim.shim_plan(ctypes.byref(a), out)
-            if max(m, n) * 512 * -(-k // 512) > 1 << 40 or m * 512 * -(-n // 512) > 1 << 40:
+            pad = [128 * -(-v // 128) for v in (m, n, k)]
+            if max(m, n) * pad[2] > 1 << 35 or m * pad[1] > 1 << 35 or n * pad[0] > 1 << 35:
                 assert st != 0
                 continue
             assert st == 0
@@ -182,6 +183,13 @@ def test_products_are_planned_within_their_limits(mx, shim):
                 assert parts % 256 == 0 and parts >= a_scales + m * scales
             else:
                 assert parts == 0
+            # what a launch counts stays below 2^32 threads
+            if shape == 0:
+                assert -(-n // 16) * 512 < 1 << 32
+            else:
+                edge, threads = (128, 256) if shape == 1 else (256, 512)
+                assert -(-m // edge) * -(-n // edge) * threads < 1 << 32
+                assert splits == 1 or m * -(-n // 4) < 1 << 32
             if shape:
                 units = -(-k // 256)
                 assert splits >= 1 and per >= 1 and (splits - 1) * per < units <= splits * per
