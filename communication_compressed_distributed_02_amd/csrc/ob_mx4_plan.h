@@ -109,7 +109,7 @@ inline ob_status check_average(const void* const* codes, const void* const* scal
 }
 
 // How a product is computed, from its sizes and types alone.
-enum Shape { kNarrow, kTiles128, kTiles256 };
+enum Shape { kNarrow, kTiles128, kTiles256, kTiles128Deep };  // Deep: four units in LDS
 struct Product {
   bool empty;              // nothing to compute
   bool quantize;           // a is quantised into the workspace first
@@ -126,11 +126,16 @@ constexpr int kNarrowLds = 32 * 1024;  // bytes of LDS that it uses at most
 constexpr int64_t kNarrowElems = 24 * 1024;
 inline int64_t narrow_lds(int64_t m, int64_t k) { return m * (padded(k) / 128 * 72 + 24); }
 
+// Units from which a block alone on its CU holds four of them in LDS and not two,
+// so that the loads of three are on their way: 1600 x 1600 x 16384, 64 units, 40.3
+// us, with two 50.9; 16 units of 4096 x 1024 15.2 and 17.1; 12 of 1200 x 2000 12.2
+// and 11.9, 8 of 2048 x 2048 9.7 and 9.5.
+constexpr int kDeepUnits = 16;
 // Tiles of 128 x 128 or 256 x 256, and into how many parts the sum goes: the
 // shortest by an estimate in ns, a round of tiles at a time.  The figures are
 // those of 8192 x 8192 x 16384 (both shapes) and of short sums; the choices
-// against all others, in us: 4096 x 1024 x 4096 15.6, next 26.1; 8192 x 8192 x
-// 16384 484, 631; 300 x 1000 x 16384 in 8 parts 17, 20 in 4, 37 in one.
+// against all others, in us: 4096 x 1024 x 4096 15.2, next 25.3; 8192 x 8192 x
+// 16384 484, 631; 300 x 1000 x 16384 in 8 parts 17, 19 in 4, 38 in one.
 inline double choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
   struct Cost {
     Shape shape;
@@ -148,13 +153,15 @@ inline double choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
       const int64_t real = (units + per - 1) / per;
       if (splits > 1 && (real < splits || tiles * splits > c.slots)) break;
       const double rounds = (double)((tiles * real + c.slots - 1) / c.slots);
-      // a block that has its CU to itself is faster
-      const double alone = c.slots == 512 && tiles * real <= 256 ? 0.55 : 1.0;
-      double t = rounds * ((double)per * c.unit * alone + c.fixed);
+      // a block that has its CU to itself is faster, and over a long sum faster
+      // still with more units on their way
+      const bool alone = c.slots == 512 && tiles * real <= 256, deep = alone && per >= kDeepUnits;
+      double t = deep ? (double)per * 520.0 + 5000.0
+                      : rounds * ((double)per * c.unit * (alone ? 0.55 : 1.0) + c.fixed);
       if (real > 1) t += 3000.0 + (double)(m * n) * (real * 8.0 + 2.0) / 4000.0;
       if (best == 0.0 || t < best) {
         best = t;
-        p->shape = c.shape;
+        p->shape = deep ? kTiles128Deep : c.shape;
         p->splits = (int)real;
         p->per_split = (int)per;
       }
@@ -163,7 +170,7 @@ inline double choose_tiles(int64_t m, int64_t n, int64_t k, Product* p) {
   return best;
 }
 // What the narrow kernel takes: b's bytes at 4 TB/s, and more the more rows of a.
-// One row of 16384 x 16384 36 us (tiles 26), 16 rows 58 (28); of 4096 x 4096 4.4
+// One row of 16384 x 16384 36 us (tiles 26), 16 rows 58 (27); of 4096 x 4096 4.4
 // (8.3) and 5.8 (9.5), 64 rows 11.1 (11.0).
 inline double narrow_time(int64_t m, int64_t n, int64_t k) {
   return 2500.0 + (double)n * row_codes(k) * (0.246e-3 + 0.0124e-3 * m);

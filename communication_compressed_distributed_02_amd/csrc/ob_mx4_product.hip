@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
 // Large products.  A block of WM x WN waves takes a tile of TM x TN, each wave
 // MT x NT of the instruction's tiles, so that a 16-byte read from LDS feeds NT (or
 // MT) instructions.  Codes come into LDS by direct loads in units of 256 elements
-// (whole lines of 128 bytes), two units deep, scales for two units at a time, 16
+// (whole lines of 128 bytes), STAGES units deep, scales for two units at a time, 16
 // bytes a row.  A unit is multiplied in four steps of 64 elements; during each
 // the next one's registers are read.  At the end of the third step a unit is
 // in registers altogether: one barrier, behind which the next unit is there and
-// the unit after it may be loaded over this one.  A row's eight 16-byte pieces
+// the one STAGES behind may be loaded over this one.  A row's eight 16-byte pieces
 // lie in LDS permuted by (row / 2) % 8: lanes of consecutive rows that read the
 // same piece then meet all banks evenly.  The permutation is made by the
 // addresses that the lanes load from, since direct loads write LDS in the order
@@ -203,19 +203,22 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
 // ones); without its loads the kernel takes 375-390.  With units of 128 elements,
 // half a line each, it took 577, and 514 once the loads and reads were spread
 // among the products.  128 x 128 (4 waves of 64 x 64, two blocks on a CU) moves
-// twice as much into LDS: 623.  Short sums are bound by writing out: 16384 x
+// twice as much into LDS: 623.  Where there is one block of those for a CU at most
+// and the sum is long, four units lie in LDS and three of them are on their way, for
+// a unit takes less time there than a load: 1600 x 1600 x 16384 40 us, with two 51.  Short sums are bound by writing out: 16384 x
 // 6400 x 1600 117 us, 210 MB of them.  Results that went out from the registers,
 // in pieces of 32 bytes: 133; blocks that went on from tile to tile: 117.
-template <int WM_, int WN_, int MT_, int NT_>
+template <int WM_, int WN_, int MT_, int NT_, int STAGES_>
 struct Tile {
   static constexpr int WM = WM_, WN = WN_, MT = MT_, NT = NT_;
+  static constexpr int STAGES = STAGES_;  // units in LDS
   static constexpr int TM = WM * MT * 32, TN = WN * NT * 32, WAVES = WM * WN;
   static constexpr int LA = TM / 8 / WAVES, LB = TN / 8 / WAVES;  // loads of a unit, a wave
   static constexpr int SCALE_CHUNKS = (TM + TN) / 64;             // loads of two units' scales
   static constexpr int LS = (SCALE_CHUNKS + WAVES - 1) / WAVES;
   static constexpr int UNIT = (TM + TN) * 128, SCALES = (TM + TN) * 16;
   static constexpr int STRIP = NT * 32 + 4;  // floats of a row on the way out
-  static constexpr int LOOP_BYTES = 2 * UNIT + 2 * SCALES;
+  static constexpr int LOOP_BYTES = STAGES * (UNIT + SCALES);
   static constexpr int OUT_BYTES = WAVES * 32 * STRIP * 4;
   static constexpr int LDS = LOOP_BYTES > OUT_BYTES ? LOOP_BYTES : OUT_BYTES;
   static_assert(LA % 2 == 0 && LB % 2 == 0 && TM % (8 * WAVES) == 0 && TN % (8 * WAVES) == 0, "");
@@ -234,9 +237,22 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
       : "s"(lds), "v"(offset), "s"(base), "s"(lanes)
       : "memory");
 }
-// This wave's reads and loads are done, and so are those of all the block's waves.
-__device__ __forceinline__ void arrived() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// This wave's reads are done, and its loads but for the last N, and so are those of
+// all the block's waves.  Not `steady` (uniform): all loads, since some of the last N
+// may have had no lanes.  The branch stays in here, unseen by the compiler, which would
+// move products past it.
+template <int N>
+__device__ __forceinline__ void arrived(bool steady) {
+  if constexpr (N == 0) {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  } else {
+    const int s = __builtin_amdgcn_readfirstlane(steady ? 1 : 0);
+    asm volatile(
+        "s_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 1f\n\ts_waitcnt vmcnt(0)\n1:\n\t"
+        "s_waitcnt vmcnt(%1) lgkmcnt(0)\n\ts_barrier" ::"s"(s),
+        "n"(N)
+        : "memory", "scc");
+  }
 }
 // A uniform 64-bit value in scalar registers.
 __device__ __forceinline__ uint64_t uniform(uint64_t x) {
@@ -306,12 +322,12 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
   // behind the last unit none, and no branch is needed.
   constexpr int kLoads = C::LS + C::LA + C::LB;
   const auto load = [&](int u, int i) {
-    const uint32_t to = lds0 + (u & 1) * C::UNIT;
+    const uint32_t to = lds0 + u % C::STAGES * C::UNIT;
     if (i < C::LS) {
       const int chunk = wave * C::LS + i;
       const bool wanted = !(u & 1) && u < units && chunk < C::SCALE_CHUNKS;
       load_to_lds((chunk < C::TM / 64 ? a_scales : b_scales) + u * 8, from_s[i],
-                  lds0 + 2 * C::UNIT + (u >> 1 & 1) * C::SCALES + chunk * 1024,
+                  lds0 + C::STAGES * C::UNIT + (u >> 1) % C::STAGES * C::SCALES + chunk * 1024,
                   uniform(wanted ? ~uint64_t(0) : 0));
       return;
     }
@@ -336,7 +352,7 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
   constexpr int kReads = C::MT + C::NT;
   const auto read = [&](int u, int h, int i, Step* f) {
     const uint8_t* from =
-        lds + (u & 1) * C::UNIT + row * 128 + (((2 * h + half) ^ (row >> 1 & 7)) * 16);
+        lds + u % C::STAGES * C::UNIT + row * 128 + (((2 * h + half) ^ (row >> 1 & 7)) * 16);
     if (i < C::MT)
       f->a[i] = *(const u32x4*)(from + (wm * C::MT + i) * 4096);
     else
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
   };
   const auto read_scale = [&](int u, int i, Scales* s) {
     const uint8_t* from =
-        lds + 2 * C::UNIT + (u >> 1 & 1) * C::SCALES + row * 16 + (u & 1) * 8;
+        lds + C::STAGES * C::UNIT + (u >> 1) % C::STAGES * C::SCALES + row * 16 + (u & 1) * 8;
     if (i < C::MT)
       s->a[i] = *(const u32x2*)(from + (wm * C::MT + i) * 512);
     else
@@ -399,7 +415,7 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
       else if (k < 2 * kReads)
         read(u + 1, 0, k - kReads, &f0);
       else
-        load(u + 2, k - 2 * kReads);
+        load(u + C::STAGES, k - 2 * kReads);
     });
     s0 = shifted(s1);
   };
@@ -408,7 +424,7 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
       if (k < kReads)
         read(u, 1, k, &f1);
       else
-        load(u + 1, k - kReads + kL1);
+        load(u + C::STAGES - 1, k - kReads + kL1);
     });
   };
   const auto step1 = [&](int u) {
@@ -418,15 +434,21 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
     multiply_step(k2, f0, s0, kOnlyReads, [&](int k) { read(u, 3, k, &f1); });
   };
 
+  // loads of codes of the units that may be in flight behind the one awaited; those
+  // of scales are left out, as not every unit and wave has them
+  constexpr int kBehind = (C::STAGES - 2) * (C::LA + C::LB);
+  const auto await = [&](int u) { arrived<kBehind>(u + C::STAGES - 2 < units); };
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) load(0, i);
-  arrived();
+  for (int u = 0; u < C::STAGES - 1; ++u)
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(u, i);
+  await(0);
 #pragma unroll
   for (int i = 0; i < kReads; ++i) read_scale(0, i, &s1);
 #pragma unroll
   for (int i = 0; i < kReads; ++i) read(0, 0, i, &f0);
 #pragma unroll
-  for (int i = 0; i < kL1; ++i) load(1, i);
+  for (int i = 0; i < kL1; ++i) load(C::STAGES - 1, i);
   s0 = shifted(s1);
   __builtin_amdgcn_sched_barrier(0);
   step0(0);
@@ -436,20 +458,20 @@ __global__ void __launch_bounds__(C::WAVES * 64) tile_kernel(ProductArgs p, uint
     step2(0);
 #pragma unroll 1
     for (int u = 0; u + 1 < full; ++u) {
-      arrived();
+      await(u + 1);
       step3(u);
       step0(u + 1);
       step1(u + 1);
       step2(u + 1);
     }
-    arrived();
+    await(full);
     step3(full - 1);  // behind the last unit what it reads is not used
     if (odd) {
       step0(full);
       step1(full);
     }
   }
-  arrived();
+  arrived<0>(true);
   // Out by strips of 32 rows through this wave's part of LDS, 16 bytes a lane.
   float* strip = (float*)lds + wave * 32 * C::STRIP;
   constexpr int kWide = sizeof(T) == 2 ? 8 : 4;  // results a lane stores
@@ -504,8 +526,9 @@ hipError_t tiles(const ProductArgs& p, int splits, int per_split, hipStream_t st
 }
 template <typename T>
 hipError_t tiles(const ProductArgs& p, Shape shape, int splits, int per_split, hipStream_t stream) {
-  return shape == kTiles256 ? tiles<T, Tile<2, 4, 4, 2>>(p, splits, per_split, stream)
-                            : tiles<T, Tile<2, 2, 2, 2>>(p, splits, per_split, stream);
+  if (shape == kTiles256) return tiles<T, Tile<2, 4, 4, 2, 2>>(p, splits, per_split, stream);
+  if (shape == kTiles128) return tiles<T, Tile<2, 2, 2, 2, 2>>(p, splits, per_split, stream);
+  return tiles<T, Tile<2, 2, 2, 2, 4>>(p, splits, per_split, stream);
 }
 
 template <typename T>

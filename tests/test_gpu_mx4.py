@@ -268,12 +268,17 @@ LARGE = [(65, 70, 5000), (70, 5000, 130), (300, 260, 8200), (2100, 2051, 300), (
 FEW = [(1, 6400, 1600), (4, 1600, 6400), (16, 17, 16384), (24, 1000, 1024), (25, 1000, 1024), (64, 33, 129),
        (64, 1024, 4096), (64, 6000, 6000), (33, 16, 20000), (2, 9000, 9000)]
 
+# sums of 16 units and more in tiles that have a compute unit each: 16 units, 16 and
+# a half, one more, 32, and in four parts of 20, the last of them shorter
+LONG = [(1537, 1500, 4096), (1600, 1333, 4200), (2049, 1800, 4300), (1601, 1500, 8191),
+        (257, 2000, 20000)]
+
 
 @pytest.mark.parametrize("raw", [None, "bf16"])
 def test_large_products_of_integers_are_exact(mx, raw):
     """Sizes that take each shape of tile, whole and at its edges, one unit of
     the sum, an odd half of one, and sums in several parts."""
-    for i, (m, n, k) in enumerate(LARGE + FEW):
+    for i, (m, n, k) in enumerate(LARGE + FEW + LONG):
         a, b = gpu(integers(m, k, i)), gpu(integers(n, k, 50 + i))
         want = a.double() @ b.double().t()
         qa = mx.quantize(a) if raw is None else a.to(DT[raw])
@@ -292,7 +297,8 @@ def test_large_products_of_integers_are_exact(mx, raw):
         log("%d x %d x %d" % (m, n, k))
 
 
-@pytest.mark.parametrize("m, n, k", [(300, 300, 4000), (4097, 2305, 1200), (40, 700, 3000)])
+@pytest.mark.parametrize("m, n, k", [(300, 300, 4000), (4097, 2305, 1200), (40, 700, 3000),
+                                     (1537, 1500, 5000)])
 def test_large_products_of_spread_values(mx, m, n, k):
     x, w = gpu(ref.spread(m, k, 1)), gpu(ref.spread(n, k, 2))
     qx, qw = mx.quantize(x), mx.quantize(w)

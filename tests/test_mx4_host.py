@@ -187,7 +187,8 @@ def test_products_are_planned_within_their_limits(mx, shim):
             if shape == 0:
                 assert -(-n // 16) * 512 < 1 << 32
             else:
-                edge, threads = (128, 256) if shape == 1 else (256, 512)
+                edge, threads = (256, 512) if shape == 2 else (128, 256)
+                assert shape != 3 or (splits * -(-m // 128) * -(-n // 128) <= 256 and per >= 16)
                 assert -(-m // edge) * -(-n // edge) * threads < 1 << 32
                 assert splits == 1 or m * -(-n // 4) < 1 << 32
             if shape:
