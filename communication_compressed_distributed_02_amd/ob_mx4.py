@@ -164,12 +164,15 @@ class MX4:
     def _like(cls, x, rows, cols):
         """One with undefined contents where the tensor x lies: codes and scales
         in one allocation, made views of when they are asked for."""
+        return cls._over(x.new_empty(rows * sum(_widths(cols)), dtype=torch.uint8), rows, cols)
+
+    @classmethod
+    def _over(cls, held, rows, cols):
+        """One whose codes and then scales fill `held`."""
         q = object.__new__(cls)
-        c, s = _widths(cols)
-        held = x.new_empty(rows * (c + s), dtype=torch.uint8)
         q.rows, q.cols, q.device, q._held = rows, cols, held.device, held
         q.code_ptr = held.data_ptr()
-        q.scale_ptr = q.code_ptr + rows * c
+        q.scale_ptr = q.code_ptr + rows * _widths(cols)[0]
         return q
 
     def _part(self, i):
@@ -421,27 +424,34 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, quantized, seed):
         need_x, need_w = ctx.needs_input_grad[:2]
         m = _unit(x)
-        ctx.quantized = quantized
+        a = x_cols = w_cols = None
         if quantized is not None:
-            w, ctx.w_cols, ctx.version = quantized.rows, quantized.cols, quantized.version
+            w, ctx.version = quantized.rows, quantized.version
         elif need_x:
-            w, ctx.w_cols = quantize_both(weight)
+            w, w_cols = quantize_both(weight)
         else:
             w = quantize(weight)
-        ctx.seed, ctx.x_shape, ctx.x_dtype, ctx.w_dtype = seed, x.shape, x.dtype, weight.dtype
-        shape = (*x.shape[:-1], weight.shape[0])
         if need_w:
-            a, ctx.x_cols = quantize_both(m)
-        elif _by_rows(m):
-            return matmul(m, w, x.dtype).view(shape)
-        else:
+            a, x_cols = quantize_both(m)
+        elif not _by_rows(m):
             a = quantize(m)
+        ctx.quantized, ctx.seed, ctx.x_shape, ctx.x_dtype = quantized, seed, x.shape, x.dtype
+        ctx.w_shape, ctx.w_dtype = weight.shape, weight.dtype
+        # as tensors of the graph's, so that it frees them behind the backward pass
+        # and hooks on saved tensors (checkpointing) have them
+        ctx.save_for_backward(None if x_cols is None else x_cols._held,
+                              None if w_cols is None else w_cols._held)
+        shape = (*x.shape[:-1], weight.shape[0])
+        if a is None:
+            return matmul(m, w, x.dtype).view(shape)
         return _of_mx4(a, w, m, x.dtype, shape)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         need_x, need_w = ctx.needs_input_grad[:2]
+        x_held, w_held = ctx.saved_tensors
+        n, k = ctx.w_shape
         if ctx.quantized is not None and ctx.quantized.version != ctx.version:
             raise RuntimeError("the weight's copies were refreshed between forward and backward")
         dy = _unit(dy)
@@ -453,9 +463,10 @@ class _Linear(torch.autograd.Function):
         elif need_w:
             g_cols = quantize(dy.t(), ctx.seed)
         if need_x:
-            dx = _of_mx4(g, ctx.w_cols, dy, ctx.x_dtype, ctx.x_shape)
+            w_cols = MX4._over(w_held, k, n) if ctx.quantized is None else ctx.quantized.cols
+            dx = _of_mx4(g, w_cols, dy, ctx.x_dtype, ctx.x_shape)
         if need_w:
-            dw = _of_mx4(g_cols, ctx.x_cols, dy, ctx.w_dtype)
+            dw = _of_mx4(g_cols, MX4._over(x_held, k, dy.shape[0]), dy, ctx.w_dtype)
         return dx, dw, None, None
 
 
@@ -467,7 +478,9 @@ def linear(x, weight, quantized=None, seed=None):
     weight's.  quantized: the weight's copies where they are kept (a Weight of it,
     as AdamWOptimizer keeps; they are not checked against it).  seed: round dy
     stochastically, as quantize; None rounds it to nearest.  What the backward pass
-    keeps of x are 4-bit columns.  Not differentiable twice."""
+    keeps of x are 4-bit columns.  Not differentiable twice.  As with all of torch, a
+    backward pass is captured in a graph only while no eager graph of the same
+    leaves is alive."""
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x of shape %s, weight of shape %s" % (tuple(x.shape), tuple(weight.shape)))
     if x.device != weight.device:

@@ -456,6 +456,42 @@ def test_linear_shapes_and_partial_gradients(mx):
         y.sum().backward()
 
 
+def test_linear_keeps_and_frees_through_the_graph(mx):
+    """What it keeps are saved tensors: freed behind the backward pass though y is
+    alive, kept on request, seen by hooks, made again under checkpointing."""
+    from torch.utils.checkpoint import checkpoint
+    m, n, k = 1000, 130, 4000
+    x = gpu(ref.spread(m, k, 1)).requires_grad_()
+    w = gpu(ref.spread(n, k, 2)).requires_grad_()
+    dy = gpu(ref.spread(m, n, 3))
+    y = mx.linear(x, w, seed=5)
+    want = torch.autograd.grad(y, (x, w), dy, retain_graph=True)
+    again = torch.autograd.grad(y, (x, w), dy)
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(y, (x, w), dy)
+    del y, again
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    y = mx.linear(x, w)
+    held = torch.cuda.memory_allocated() - before - y.nbytes
+    assert k * m // 2 <= held
+    torch.autograd.grad(y, (x, w), dy)
+    assert torch.cuda.memory_allocated() - before - y.nbytes < 4096
+    del y
+
+    packed = []
+    with torch.autograd.graph.saved_tensors_hooks(
+            lambda t: packed.append(t.nbytes) or t.cpu(), lambda t: t.cuda()):
+        y = mx.linear(x, w, seed=5)
+    assert len(packed) == 2
+    got = torch.autograd.grad(y, (x, w), dy)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    y = checkpoint(lambda a: mx.linear(a, w, seed=5), x, use_reentrant=False)
+    got = torch.autograd.grad(y, (x, w), dy)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
 def test_captured_calls_replay(mx):
     """Quantising with a seed on the device, averaging and products in a graph,
     replayed over new contents with eager work in between."""
