@@ -85,16 +85,16 @@ typedef struct {
 ob_status ob_mx4_quantize(const ob_mx4_quantize_args* args, void* stream);
 
 /* Mean of n messages (1 .. OB_MX4_MAX_MESSAGES, OB_ERR_SHAPE otherwise; 1 reads a
- * matrix back) of rows x cols.  codes, scales: host arrays of n device pointers, 16-byte aligned; they
- * may repeat.  Element (r, c) goes to out[r * stride + c], stride >= cols, of
- * type dtype. */
+ * matrix back) of rows x cols.  codes, scales: host arrays of n device pointers,
+ * 16-byte aligned; they may repeat.  Element (r, c) goes to out[r * stride + c],
+ * stride >= cols, of type dtype. */
 ob_status ob_mx4_average(const void* const* codes, const void* const* scales, int32_t n,
                          int64_t rows, int64_t cols, int32_t dtype, void* out, int64_t stride,
                          void* stream);
 
 typedef struct {
-  int64_t m, n, k;      /* out is m x n (and n x m as large as a matrix may be), a m x k, b
-                           n x k; k <= 2^24 */
+  int64_t m, n, k;      /* out is m x n, a m x k, b n x k; k <= 2^24, and the limit of elements
+                           in padded rows holds for n x m too */
   const void* a_codes;  /* 16-byte aligned; NULL with a_scales: a is given in a */
   const void* a_scales;
   const void* a;        /* element (i, k) at a[i * a_stride + k]: quantised to nearest on the way */
