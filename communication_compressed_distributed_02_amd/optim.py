@@ -165,8 +165,9 @@ class AdamWOptimizer(torch.optim.Optimizer):
     is.  quantized: matrices among the parameters whose 4-bit copies (ob_mx4.Weight)
     are kept in `quantized`, a dict by parameter, and written again by every step
     that changes them: for ob_mx4.linear and ob_mx4.matmul.  Parameters that are
-    written otherwise need refresh().  state_dict() / load_state_dict() carry the library's whole state and what it
-    was made with, all of which but grad_dtype has to be the same where it is loaded."""
+    written otherwise need refresh().  state_dict() / load_state_dict() carry the
+    library's whole state and what it was made with, all of which but grad_dtype has
+    to be the same where it is loaded."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                  state_bits=32, master=False, stochastic=False, grad_dtype=None, max_norm=0.0,
