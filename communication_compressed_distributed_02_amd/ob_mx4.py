@@ -434,6 +434,15 @@ def _of_mx4(a, b, like, dtype, shape=None):
     return c if shape is None or len(shape) == 2 else c.view(shape)
 
 
+def _forward(x, m, a, w):
+    """The layer's output: of a, x quantised, or where that is None of m, x as a
+    matrix by rows, which is quantised on the way."""
+    shape = (*x.shape[:-1], w.rows)
+    if a is None:
+        return matmul(m, w, x.dtype).view(shape)
+    return _of_mx4(a, w, m, x.dtype, shape)
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, quantized, seed):
@@ -456,10 +465,7 @@ class _Linear(torch.autograd.Function):
         # and hooks on saved tensors (checkpointing) have them
         ctx.save_for_backward(None if x_cols is None else x_cols._held,
                               None if w_cols is None else w_cols._held)
-        shape = (*x.shape[:-1], weight.shape[0])
-        if a is None:
-            return matmul(m, w, x.dtype).view(shape)
-        return _of_mx4(a, w, m, x.dtype, shape)
+        return _forward(x, m, a, w)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -493,7 +499,8 @@ def linear(x, weight, quantized=None, seed=None):
     weight's.  quantized: the weight's copies where they are kept (a Weight of it,
     as AdamWOptimizer keeps; they are not checked against it).  seed: round dy
     stochastically, as quantize; None rounds it to nearest.  What the backward pass
-    keeps of x are 4-bit columns.  Not differentiable twice.  As with all of torch, a
+    keeps of x are 4-bit columns; without gradients (torch.no_grad) none are made.
+    Not differentiable twice.  As with all of torch, a
     backward pass is captured in a graph only while no eager graph of the same
     leaves is alive."""
     if weight.dim() != 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
@@ -508,4 +515,9 @@ def linear(x, weight, quantized=None, seed=None):
                                   or quantized.rows.device != weight.device):
         raise ValueError("quantized is of a weight of %d x %d on %s"
                          % (*quantized.rows.shape, quantized.rows.device))
+    if not torch.is_grad_enabled():
+        # needs_input_grad would go by requires_grad alone
+        m = _unit(x)
+        return _forward(x, m, None if _by_rows(m) else quantize(m),
+                        quantize(weight) if quantized is None else quantized.rows)
     return _Linear.apply(x, weight, quantized, seed)
