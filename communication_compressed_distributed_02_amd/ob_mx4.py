@@ -111,11 +111,14 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 def _on(device, fn, *args):
     """fn(*args, stream) with `device` current, on its current stream."""
-    if _current_device() != device.index:
+    index = device.index  # None off the GPU
+    if index is None or _current_device() != index:
+        if device.type != "cuda":
+            raise ValueError("a quantised matrix on %s: a GPU is needed" % device)
         with torch.cuda.device(device):
-            fn(*args, _current_stream(device.index))
+            fn(*args, _current_stream(index))
     else:
-        fn(*args, _current_stream(device.index))
+        fn(*args, _current_stream(index))
 
 
 def _widths(cols):
@@ -150,7 +153,7 @@ class MX4:
         if codes.device != scales.device:
             raise ValueError("codes on %s, scales on %s" % (codes.device, scales.device))
         # aliases, which stay there should the caller's be given other memory
-        self.__setstate__((codes.shape[0], cols, (codes.detach(), scales.detach())))
+        self._place(codes.shape[0], cols, (codes.detach(), scales.detach()))
 
     @classmethod
     def empty(cls, rows, cols, device):
@@ -170,7 +173,7 @@ class MX4:
     def _over(cls, held, rows, cols):
         """One whose codes and then scales fill `held`."""
         q = object.__new__(cls)
-        q.__setstate__((rows, cols, held))
+        q._place(rows, cols, held)
         return q
 
     # What is copied or sent are the tensors alone: where they lie is read off the
@@ -180,7 +183,10 @@ class MX4:
         return self.rows, self.cols, self._held
 
     def __setstate__(self, state):
-        self.rows, self.cols, self._held = rows, cols, held = state
+        self._place(*state)
+
+    def _place(self, rows, cols, held):
+        self.rows, self.cols, self._held = rows, cols, held
         if isinstance(held, tuple):
             self.device = held[0].device
             self.code_ptr, self.scale_ptr = held[0].data_ptr(), held[1].data_ptr()
@@ -334,7 +340,6 @@ def average(messages, dtype=torch.float32, out=None):
     if not messages:
         raise ValueError("no messages")
     first = messages[0]
-    _need_gpu(first, "a message")
     for q in messages[1:]:
         if q.rows != first.rows or q.cols != first.cols or q.device != first.device:
             raise ValueError("messages differ: %r and %r" % (first, q))
@@ -367,7 +372,6 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
     to nearest on the way (its dimensions in front of the last are those of the
     result).  out: a matrix to write to; accumulate: add to it."""
     if isinstance(a, MX4):
-        _need_gpu(a, "a")
         shape, rows, cols, device = None, a.rows, a.cols, a.device
         given = a.code_ptr, a.scale_ptr, None, 0
         stride = 0
