@@ -17,6 +17,7 @@ in the library's HIP kernels; there is no fallback.
 """
 import ctypes
 import math
+import weakref
 
 import torch
 
@@ -412,17 +413,40 @@ def _product(given, stride, rows, cols, b, c, dtype, accumulate=False):
 class Weight:
     """A weight's 4-bit copies: `rows` (N x K) for the forward product, `cols` (K x N)
     for the gradient of the input."""
-    __slots__ = ("rows", "cols", "version")
+    # _of, _seen: the tensor they were written from, and where it lay and its count of
+    # writes then.  Not copied or sent along: another tensor counts otherwise.
+    __slots__ = ("rows", "cols", "version", "_of", "_seen")
 
     def __init__(self, weight):
         self.rows, self.cols = quantize_both(weight.detach())
         self.version = 0
+        self._of, self._seen = weakref.ref(weight), _writes(weight)
 
     def refresh(self, weight):
         """Written again, where they lie, from the weight as it is now."""
         quantize_both(weight.detach(), out=(self.rows, self.cols))
         self.version += 1
+        self._of, self._seen = weakref.ref(weight), _writes(weight)
         return self
+
+    def __getstate__(self):
+        return self.rows, self.cols, self.version
+
+    def __setstate__(self, state):
+        self.rows, self.cols, self.version = state
+        self._of = self._seen = None
+
+    def behind(self, weight):
+        """Whether `weight` is the tensor that they were written from and was written
+        or moved since, as far as torch counts: writes through .data and by replays of
+        a graph are not.  Of a Weight that was copied or loaded nothing is known."""
+        return (self._of is not None and self._of() is weight
+                and self._seen != _writes(weight))
+
+
+def _writes(t):
+    """Where a tensor lies and torch's count of the writes to it."""
+    return t.data_ptr(), None if t.is_inference() else t._version
 
 
 def _unit(x):
@@ -500,8 +524,8 @@ def linear(x, weight, quantized=None, seed=None):
     y = Q(x) Q(w)^T, dx = Q(dy) Q(w^T)^T, dw = Q(dy^T) Q(x^T)^T.
 
     x: [..., K], weight: [N, K], float32 or bfloat16; y and dx have x's type, dw
-    weight's.  quantized: the weight's copies where they are kept (a Weight of it,
-    as AdamWOptimizer keeps; they are not checked against it).  seed: round dy
+    weight's.  quantized: the weight's copies where they are kept (a Weight of it, as
+    AdamWOptimizer keeps): RuntimeError where they are `behind` it.  seed: round dy
     stochastically, as quantize; None rounds it to nearest.  What the backward pass
     keeps of x are 4-bit columns; without gradients (torch.no_grad) none are made.
     Not differentiable twice.  As with all of torch, a
@@ -519,6 +543,9 @@ def linear(x, weight, quantized=None, seed=None):
                                   or quantized.rows.device != weight.device):
         raise ValueError("quantized is of a weight of %d x %d on %s"
                          % (*quantized.rows.shape, quantized.rows.device))
+    if quantized is not None and quantized.behind(weight):
+        raise RuntimeError("the weight was written or moved since its 4-bit copies were: refresh() "
+                           "them")
     if not torch.is_grad_enabled():
         # needs_input_grad would go by requires_grad alone
         m = _unit(x)
