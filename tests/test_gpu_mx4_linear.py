@@ -159,3 +159,19 @@ def test_the_optimizers_copies_are_told_from_loaded_weights(mx):
     w.grad = torch.zeros_like(w)
     opt.step()
     assert torch.equal(mx.linear(x, w, kept), mx.linear(x, w))
+
+
+def test_a_refresh_in_between_matters_to_the_gradient_of_x_alone(mx):
+    w = torch.nn.Parameter(gpu(ref.spread(40, 70, 1)))
+    x, dy = gpu(ref.spread(9, 70, 2)), gpu(ref.spread(9, 40, 3))
+    kept = mx.Weight(w)
+    want, = torch.autograd.grad(mx.linear(x, w), w, dy)
+    y = mx.linear(x, w, kept)
+    kept.refresh(w)
+    got, = torch.autograd.grad(y, w, dy)  # does not read the copies
+    assert torch.equal(got, want)
+    y = mx.linear(x.requires_grad_(), w, kept)
+    kept.refresh(w)
+    for of in (x, (x, w)):
+        with pytest.raises(RuntimeError, match="refreshed"):
+            torch.autograd.grad(y, of, dy, retain_graph=True)
