@@ -10,6 +10,9 @@ products, and a linear layer made of them.
     y = matmul(a, b)                    # a b^T on the matrix cores; a may be a plain tensor
     y = linear(x, weight, seed=t)       # differentiable; all three products in 4 bits
 
+Gradients pass through linear alone: while they are recorded, an input of matmul
+and tensors that are written may not want one.  An MX4 holds values only.
+
 Functions work on the current stream of their tensors' device, as torch's own
 do, and may be captured in a graph.  They raise ValueError on tensors that do
 not fit and ObAdamError on a status other than OB_OK.  Every computation runs
@@ -242,6 +245,12 @@ def _matrix(x, what):
                          % (what, tuple(x.shape), x.stride())) from None
 
 
+def _no_gradient(t, what):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("no gradient passes through %s, which wants one: detach it, or use linear"
+                         % what)
+
+
 def _by_rows(x):
     return x.stride(1) == 1 or x.shape[1] <= 1
 
@@ -295,6 +304,7 @@ def quantize(x, seed=None, residual=None, out=None):
                 or residual.device != x.device or not residual.is_contiguous()):
             raise ValueError("the residual must be a contiguous float32 tensor of x's shape on %s"
                              % x.device)
+        _no_gradient(residual, "the residual")
         if flip:
             raise ValueError("with a residual, x must be contiguous along its last dimension")
     out = _target(out, m.shape[0], m.shape[1], x, "out")
@@ -332,6 +342,7 @@ def _result(out, rows, cols, dtype, device):
             or not _by_rows(out) or (rows > 1 and out.stride(0) < cols)):
         raise ValueError("out must be %d x %d of %s on %s, rows contiguous and apart"
                          % (rows, cols, dtype, device))
+    _no_gradient(out, "out")
     return out
 
 
@@ -378,6 +389,7 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
         stride = 0
     else:
         m = _matrix(a, "a")
+        _no_gradient(a, "a")
         if not _by_rows(m):
             raise ValueError("a has strides %s: its last dimension must be contiguous"
                              % (m.stride(),))
