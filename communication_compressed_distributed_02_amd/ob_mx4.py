@@ -251,6 +251,19 @@ def _no_gradient(t, what):
                          % what)
 
 
+# (a half of the time of torch.autograd.graph.increment_version, which calls it)
+_count_write = getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
+def _wrote(t):
+    """Count a call's write to a tensor, or to a pair of them, as torch counts its own."""
+    if isinstance(t, tuple):
+        for part in t:
+            _wrote(part)
+    elif not t.is_inference():
+        _count_write((t,))
+
+
 def _by_rows(x):
     return x.stride(1) == 1 or x.shape[1] <= 1
 
@@ -307,11 +320,15 @@ def quantize(x, seed=None, residual=None, out=None):
         _no_gradient(residual, "the residual")
         if flip:
             raise ValueError("with a residual, x must be contiguous along its last dimension")
-    out = _target(out, m.shape[0], m.shape[1], x, "out")
+    given, out = out, _target(out, m.shape[0], m.shape[1], x, "out")
     if flip:
         _quantize(m.t(), seed, None, None, out)
     else:
         _quantize(m, seed, residual, out, None)
+    if residual is not None:
+        _wrote(residual)
+    if given is not None:
+        _wrote(given._held)
     return out
 
 
@@ -329,6 +346,9 @@ def quantize_both(x, seed=None, out=None):
         _quantize(m.t(), seed, None, cols, rows)
     else:
         _quantize(m, seed, None, rows, cols)
+    if out is not None:
+        _wrote(rows._held)
+        _wrote(cols._held)
     return rows, cols
 
 
@@ -355,10 +375,12 @@ def average(messages, dtype=torch.float32, out=None):
     for q in messages[1:]:
         if q.rows != first.rows or q.cols != first.cols or q.device != first.device:
             raise ValueError("messages differ: %r and %r" % (first, q))
-    out = _result(out, first.rows, first.cols, dtype, first.device)
+    given, out = out, _result(out, first.rows, first.cols, dtype, first.device)
     _on(first.device, ob_mx4_average, [q.code_ptr for q in messages],
         [q.scale_ptr for q in messages], first.rows, first.cols, _TYPES[dtype],
         out.data_ptr(), _row_stride(out))
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -403,6 +425,8 @@ def matmul(a, b, dtype=torch.bfloat16, out=None, accumulate=False):
         raise ValueError("accumulate needs out")
     c = _result(out, rows, b.rows, dtype, device)
     _product(given, stride, rows, cols, b, c, dtype, accumulate)
+    if out is not None:
+        _wrote(out)
     if shape is not None and len(shape) != 1 and out is None:
         return c.view(*shape, b.rows)
     return c

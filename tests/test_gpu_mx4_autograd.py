@@ -46,3 +46,52 @@ def test_a_product_does_not_lose_a_gradient(mx):
     a, b = mx.quantize_both(x)
     assert torch.equal(mx.matmul(a, w, torch.float32), want)
     assert mx.linear(x, torch.nn.Parameter(gpu(ref.spread(40, 70, 1)))).requires_grad
+
+
+def test_what_calls_write_counts_as_written(mx):
+    """A tensor that another operation kept for its backward pass and that a call
+    overwrites is told there, as torch's own writes are."""
+    x, q = gpu(ref.spread(9, 70, 1)), mx.quantize(gpu(ref.spread(40, 70, 2)))
+    v = torch.ones((), device="cuda", requires_grad=True)
+    calls = {
+        (9, 40): [lambda t: mx.matmul(x, q, torch.float32, out=t),
+                  lambda t: mx.matmul(x[:3], q, torch.float32, out=t[2:5], accumulate=True)],
+        (40, 70): [lambda t: mx.average((q, q), out=t), lambda t: q.dequantize(out=t)],
+        (9, 70): [lambda t: mx.quantize(x, residual=t)],
+    }
+    for shape, some in calls.items():
+        for call in some:
+            t = torch.ones(shape, device="cuda")
+            y = (v * t).sum()
+            call(t)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+            # a new one is untouched
+            y = (v * t).sum()
+            y.backward()
+    # a matrix that is written again, and one over the caller's tensors
+    flat = mx.quantize(x)
+    parts = mx.MX4(flat.codes.clone(), flat.scales.clone(), 70)
+    for out in (flat, parts):
+        codes, scales = out.codes, out.scales
+        seen = codes._version, scales._version
+        mx.quantize(x, out=out)
+        assert codes._version > seen[0] and scales._version > seen[1]
+    # tensors that count nothing
+    with torch.inference_mode():
+        t, e = torch.empty(40, 70, device="cuda"), torch.zeros(9, 70, device="cuda")
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            assert torch.equal(q.dequantize(out=t), q.dequantize())
+            mx.quantize(x, residual=e)
+
+
+def test_a_write_in_between_is_told_by_copies_of_it(mx):
+    """A weight that dequantize or matmul writes is one that its copies are behind."""
+    w = torch.nn.Parameter(gpu(ref.spread(40, 70, 1)))
+    x, kept, q = gpu(ref.spread(9, 70, 2)), mx.Weight(w), mx.quantize(gpu(ref.spread(40, 70, 3)))
+    with torch.no_grad():
+        q.dequantize(out=w)
+    with pytest.raises(RuntimeError, match="refresh"):
+        mx.linear(x, w, kept)
+    assert torch.equal(mx.linear(x, w, kept.refresh(w)), mx.linear(x, w))
