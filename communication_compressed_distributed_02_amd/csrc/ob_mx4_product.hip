@@ -226,7 +226,11 @@ struct Tile {
 };
 
 // 16 bytes of each of the lanes in `lanes` (uniform) from base + offset into LDS
-// at `lds`, in the lanes' order.  With no lane it moves nothing.
+// at `lds`, in the lanes' order.  With no lane it moves nothing.  m0 is named as
+// written, so that no use of the compiler's own is moved around it; that it is not
+// preserved, of which the compiler warns, is what is meant.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds,
                                             uint64_t lanes) {
   uint64_t all;
@@ -235,8 +239,9 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
       "global_load_lds_dwordx4 %2, %3\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
       : "s"(lds), "v"(offset), "s"(base), "s"(lanes)
-      : "memory");
+      : "memory", "m0");
 }
+#pragma clang diagnostic pop
 // This wave's reads are done, and its loads but for the last N, and so are those of
 // all the block's waves.  Not `steady` (uniform): all loads, since some of the last N
 // may have had no lanes.  The branch stays in here, unseen by the compiler, which would
