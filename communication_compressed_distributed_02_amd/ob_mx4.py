@@ -5,10 +5,10 @@ products, and a linear layer made of them.
     q = quantize(x)                     # x: float32 or bfloat16, blocks along its last dimension
     rows, cols = quantize_both(x)       # x and its transpose, from one read
     q.dequantize()                      # back to float32 or bfloat16
-    msg = quantize(g, seed=t, residual=e)      # a worker's message, with error feedback
+    msg = quantize(g, seed=s, residual=e)      # a worker's message, with error feedback
     mean = average(messages)            # of several workers
     y = matmul(a, b)                    # a b^T on the matrix cores; a may be a plain tensor
-    y = linear(x, weight, seed=t)       # differentiable; all three products in 4 bits
+    y = linear(x, weight, seed=s)       # differentiable; all three products in 4 bits
 
 Gradients pass through linear alone: while they are recorded, an input of matmul
 and tensors that are written may not want one.  An MX4 holds values only.
@@ -305,9 +305,13 @@ def quantize(x, seed=None, residual=None, out=None):
     contiguous, either one.
 
     seed: round stochastically with these random bits (a number, or an int64
-    device scalar that is read when the call runs); None rounds to nearest.
+    device scalar that is read when the call runs); None rounds to nearest.  The bits
+    go by the seed and the place in the matrix alone: every step, worker and tensor
+    needs a seed of its own, or they round alike and their errors do not average out.
     residual: contiguous float32 of x's shape, added to x and replaced by what the
-    rounding left (error feedback).  out: an MX4 to write to."""
+    rounding left (error feedback).  Where a value is not finite its block's message
+    and residual are NaN, and so are those of later messages until the residual is
+    cleared (residual.nan_to_num_(0.0)).  out: an MX4 to write to."""
     m = _matrix(x, "x")
     flip = not _by_rows(m)
     if flip and m.stride(0) != 1 and m.shape[0] > 1:
@@ -333,8 +337,8 @@ def quantize(x, seed=None, residual=None, out=None):
 
 
 def quantize_both(x, seed=None, out=None):
-    """(quantize(x), quantize(x.t())) of a matrix, from one read.  out: a pair to
-    write to."""
+    """(quantize(x), quantize(x.t())) of a matrix, from one read.  seed: as for
+    quantize.  out: a pair to write to."""
     m = _matrix(x, "x")
     flip = not _by_rows(m)
     if flip and m.stride(0) != 1 and m.shape[0] > 1:
@@ -563,7 +567,8 @@ def linear(x, weight, quantized=None, seed=None):
     x: [..., K], weight: [N, K], float32 or bfloat16; y and dx have x's type, dw
     weight's.  quantized: the weight's copies where they are kept (a Weight of it, as
     AdamWOptimizer keeps): RuntimeError where they are `behind` it.  seed: round dy
-    stochastically, as quantize; None rounds it to nearest.  What the backward pass
+    stochastically, as quantize, another one for every layer and step; None rounds it
+    to nearest.  What the backward pass
     keeps of x are 4-bit columns; without gradients (torch.no_grad) none are made.
     Not differentiable twice.  As with all of torch, a
     backward pass is captured in a graph only while no eager graph of the same

@@ -23,10 +23,12 @@
  *    below 4 and 2 from there; the code's magnitude is y / g rounded to
  *    nearest even, or floor(y / g + u / 65536), times g; it keeps c's sign.
  *    New residual: c - value, rounded once.  A block that holds a c that is
- *    not finite gets E = 255 and codes of zero, its residuals become NaN.
+ *    not finite gets E = 255 and codes of zero, its residuals become NaN and,
+ *    being added to what comes next, stay so until the caller clears them.
  *  - u: 16 random bits.  Elements 4i .. 4i+3 of the padded matrix (rows of
  *    128 * ceil(cols / 128)) take the low and the high half of word 0, then of
- *    word 1, hashed from i and the seed.  Equal seeds and inputs give equal bits.
+ *    word 1, hashed from i and the seed.  Equal seeds and inputs give equal bits:
+ *    matrices whose errors have to be independent need seeds of their own.
  *  - a transposed result is the same function of the transposed matrix.
  *  - average: the values are added in the order of the messages, starting from
  *    the first, and the sum is multiplied by (float)(1.0 / n); rounded to
