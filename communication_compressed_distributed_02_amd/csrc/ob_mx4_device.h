@@ -258,14 +258,18 @@ __device__ __forceinline__ uint32_t encode8_stochastic(u32x4 w, uint32_t byte, u
   return byte == 255u ? 0u : join4(p0, p1, p2, p3);
 }
 
-// The values of 8 codes.
-__device__ __forceinline__ void decode8(uint32_t codes, float scale, float* v) {
+// 8 codes without their scale, and their values.
+__device__ __forceinline__ void grid8(uint32_t codes, float* v) {
   const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 0);
   const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 1);
   const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 2);
   const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(codes, 1.0f, 3);
-  v[0] = a.x * scale, v[1] = a.y * scale, v[2] = b.x * scale, v[3] = b.y * scale;
-  v[4] = c.x * scale, v[5] = c.y * scale, v[6] = d.x * scale, v[7] = d.y * scale;
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+}
+__device__ __forceinline__ void decode8(uint32_t codes, float scale, float* v) {
+  grid8(codes, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= scale;
 }
 
 }  // namespace mx4

@@ -108,11 +108,13 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(QuantizeArgs a)
     }
     if (RESIDUAL) {
       float v[8];
-      decode8(codes, scale_of(byte), v);
+      grid8(codes, v);
       const int64_t col = g * kLaneElems;
       float* r = a.residual + at[u].row * a.cols + col;
+      // the value itself may be 2^128, past fp32: it is subtracted as it is multiplied
+      const float scale = scale_of(byte);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c[u][i] - v[i];
+      for (int i = 0; i < 8; ++i) v[i] = __builtin_fmaf(-v[i], scale, c[u][i]);
       if (col + kLaneElems <= a.cols) {
         store8_stream(r, v);
       } else {

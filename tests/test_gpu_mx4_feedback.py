@@ -57,3 +57,23 @@ def test_seeds_next_to_each_other_round_independently(mx):
         for j in range(1, i):
             p = off[i] * off[j]
             assert p.mean().abs() <= 5 / n ** 0.5 * p.square().mean().sqrt(), (i, j)
+
+
+@pytest.mark.parametrize("seed", [None, 3])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_residuals_at_the_top_of_the_range(mx, dtype, seed):
+    """A value that rounds to 2^128 is past fp32 when it is read back, but what is
+    left of it is not: c - value, rounded once."""
+    # the largest value of the type, and some below it
+    top = np.array([torch.finfo(dtype).max, 3.5 * 2.0 ** 126, 3.4999998 * 2.0 ** 126, 3.25 * 2.0 ** 126,
+                    3.9 * 2.0 ** 126, 2.0 ** 127, 6.5 * 2.0 ** 125, 1.0, 0.0])
+    for rows in (np.tile(np.concatenate((top, -top)), (40, 2))[:, :33], top[:, None] * np.ones((1, 32))):
+        x = gpu(rows).to(dtype)
+        e = torch.zeros(rows.shape, device="cuda")
+        c = (x.float() + e).cpu().numpy()  # (a zero loses its sign)
+        q = mx.quantize(x, seed=seed, residual=e)
+        codes, scales = ref.quantize(c, seed)
+        value = ref.values(codes, scales, c.shape[1])
+        assert np.isfinite(c).all() and (np.abs(value) == 2.0 ** 128).any()
+        assert np.array_equal(q.codes.cpu().numpy(), codes) and np.array_equal(q.scales.cpu().numpy(), scales)
+        assert np.array_equal(e.cpu().numpy(), (c.astype(np.float64) - value).astype(np.float32))
