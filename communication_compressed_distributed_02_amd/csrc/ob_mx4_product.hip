@@ -228,16 +228,14 @@ struct Tile {
 // 16 bytes of each of the lanes in `lanes` (uniform) from base + offset into LDS
 // at `lds`, in the lanes' order.  With no lane it moves nothing.  m0 is named as
 // written, so that no use of the compiler's own is moved around it; that it is not
-// preserved, of which the compiler warns, is what is meant.  Five states lie in front
-// of the load, as many as a scalar register that a vector instruction wrote takes until
-// a load may read it: the compiler does not count them into a block of assembly.
+// preserved, of which the compiler warns, is what is meant.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds,
                                             uint64_t lanes) {
   uint64_t all;
   asm volatile(
-      "s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b64 exec, %4\n\ts_nop 1\n\t"
+      "s_mov_b32 m0, %1\n\ts_mov_b64 %0, exec\n\ts_mov_b64 exec, %4\n\ts_nop 0\n\t"
       "global_load_lds_dwordx4 %2, %3\n\ts_mov_b64 exec, %0"
       : "=&s"(all)
       : "s"(lds), "v"(offset), "s"(base), "s"(lanes)
