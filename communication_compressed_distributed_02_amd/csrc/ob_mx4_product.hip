@@ -198,9 +198,11 @@ __global__ void __launch_bounds__(kWaves * 64) narrow_kernel(ProductArgs p) {
 // of the lanes.
 //
 // 256 x 256 (8 waves of 128 x 64): 8192 x 8192 x 16384 in 465-485 us, 4.55-4.72
-// PFLOP/s.  The instruction alone, on random operands in registers, makes 6.2
+// PFLOP/s, with operands in the caches, in 509-547 out of memory.  The instruction alone, on random operands in registers, makes 6.2
 // (355 us): the card lowers its clock for it, from 2.4 to 1.6 GHz (9.0 on constant
-// ones); without its loads the kernel takes 375-390.  With units of 128 elements,
+// ones); without its loads the kernel takes 375-390: what separates it from the
+// instruction are loads that arrive late, the matrix pipes are busy in 62 % of the
+// cycles.  With units of 128 elements,
 // half a line each, it took 577, and 514 once the loads and reads were spread
 // among the products.  128 x 128 (4 waves of 64 x 64, two blocks on a CU) moves
 // twice as much into LDS: 623.  Where there is one block of those for a CU at most

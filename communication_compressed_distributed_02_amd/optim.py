@@ -165,7 +165,8 @@ class AdamWOptimizer(torch.optim.Optimizer):
     is.  quantized: matrices among the parameters whose 4-bit copies (ob_mx4.Weight)
     are kept in `quantized`, a dict by parameter, and written again by every step
     that changes them: for ob_mx4.linear and ob_mx4.matmul.  Parameters that are
-    written otherwise need refresh().  state_dict() / load_state_dict() carry the
+    written otherwise (load_state_dict of the model) need refresh(), for which
+    linear asks.  state_dict() / load_state_dict() carry the
     library's whole state and what it was made with, all of which but grad_dtype has
     to be the same where it is loaded."""
 

@@ -32,7 +32,8 @@
  *  - a transposed result is the same function of the transposed matrix.
  *  - average: the values are added in the order of the messages, starting from
  *    the first, and the sum is multiplied by (float)(1.0 / n); rounded to
- *    nearest even for bfloat16.
+ *    nearest even for bfloat16.  (A value of 2^128, to which c rounds from
+ *    3.5 * 2^126 on, is infinite here, not where its residual is taken.)
  *  - product: out[i][j] = sum over k of a[i][k] * b[j][k], each product exact,
  *    summed in fp32 in an order that goes by the sizes alone (equal inputs give
  *    equal bits), plus the old out with `accumulate`, rounded once to out's
